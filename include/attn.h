@@ -66,8 +66,9 @@ typedef enum {
     ATTN_ERR_LAUNCH = -7,   /* the CUDA runtime rejected a launch */
     ATTN_ERR_TIMEOUT = -8,  /* a bounded in-kernel wait ran out (device status) */
     ATTN_ERR_ARG = -9,      /* scale not finite and positive, or another bad scalar */
-    ATTN_ERR_SCRATCH = -10  /* attn_bwd_noalloc: problem exceeds the built-in scratch;
+    ATTN_ERR_SCRATCH = -10, /* attn_bwd_noalloc: problem exceeds the built-in scratch;
                                attn_sdpa_host: scratch_bytes too small */
+    ATTN_ERR_PAGE = -11     /* a page index or a length outside the cache (device status) */
 } attn_status_t;
 
 /*
@@ -241,6 +242,118 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
                     int H, int N, int d, float scale, attn_dtype_t dtype, void* stream);
 
 /*
+ * A paged key/value cache held in e4m3, with one power-of-two scale for each
+ * page and head, and softmax attention over it: the token-by-token form of
+ * attn_fwd.  (The pages have no counterpart; block-wise e4m3 with one scale
+ * per block and head is the storage of attn_fp8_quantize.)
+ *
+ * k8, v8: (num_pages, Hkv, page, d) e4m3 codes; k_scale, v_scale: (num_pages,
+ * Hkv) fp32; the value of a code is code * scale of its page and head.  page is
+ * 16, 32, 64 or 128 tokens.  page_table: (B, max_pages) int32; the token of
+ * sequence b at position t lies in slot t % page of page
+ * page_table[b][t / page].  The cache may hold more than 2^31 codes; a
+ * sequence's max_pages * page must stay below 2^31 tokens.  Codes and the
+ * 16-bit tensors are 16-byte aligned, fp32 and int32 arrays 4-byte aligned, all
+ * device memory of the current device.
+ *
+ * attn_cache_append: stores the first n_new[b] (NULL: all T) of the T new
+ * tokens of k, v (B, Hkv, T, d) of each sequence b behind the lens[b] tokens it
+ * holds.  The scale of each page and head the new tokens touch becomes the
+ * least power of two s with |x| <= 448 s for all its new values, or stays if it
+ * was larger and the page held tokens of this sequence before (slot 0 < fill);
+ * codes are e4m3(x / s), nearest even.  When the scale of a page grows, the held
+ * codes are moved to it: exact, but for codes that become subnormal, which
+ * round again.  What a page held before its first slot is written does not
+ * matter (its scale included), so pages need no clearing when they are reused;
+ * slots past the new tokens are not touched.  lens is not updated.  A page that
+ * receives tokens must belong to one sequence only (two writers of one page
+ * leave it undefined).
+ *
+ * attn_cache_attend: q (B, Hq, T, d), Hq a multiple of Hkv; query head h reads
+ * key/value head h / (Hq / Hkv).  lens[b]: tokens sequence b holds, those of
+ * the queries included; query t of its q_lens[b] (NULL: T) queries stands at
+ * position lens[b] - q_lens[b] + t and sees, when causal, the keys up to its
+ * own position, else all lens[b].  o (B, Hq, T, d) and lse (B, Hq, T) fp32 as
+ * attn_fwd writes them; a query that sees no key gets O = 0 and lse = -inf;
+ * rows t >= q_lens[b] are left as they were.  max_len: an upper bound of lens
+ * that sizes the split of long sequences over the device (a larger one costs
+ * time, a sequence longer than it is still attended to in full).  workspace:
+ * attn_cache_attend_workspace_bytes() bytes of the same sizes and max_len, 16-byte
+ * aligned (may be NULL when that is 0); its contents on entry do not matter.
+ *
+ * Errors: as attn_fwd; ATTN_ERR_ARG for another page size, max_len < 1, or K
+ * and V in one array; ATTN_ERR_SHAPE if Hkv does not divide Hq.  Contents of
+ * the int32 arrays are checked on the device: a page index outside 0 ..
+ * num_pages - 1, a length below 0 or past max_pages * page, or n_new / q_lens
+ * outside 0 .. T is never followed: its tokens are not stored (append) or not
+ * seen (attend; lengths are clamped), and attn_last_device_status() reports
+ * ATTN_ERR_PAGE.
+ */
+int attn_cache_append(const void* k, const void* v, unsigned char* k8, unsigned char* v8,
+                      float* k_scale, float* v_scale, const int* page_table, const int* lens,
+                      const int* n_new, int B, int Hkv, int T, int d, int num_pages, int page,
+                      int max_pages, attn_dtype_t dtype, void* stream);
+
+size_t attn_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int max_len);
+
+int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned char* v8,
+                      const float* k_scale, const float* v_scale, const int* page_table,
+                      const int* lens, const int* q_lens, void* o, float* lse, void* workspace,
+                      int B, int Hq, int Hkv, int T, int d, int num_pages, int page,
+                      int max_pages, int max_len, int causal, float scale, attn_dtype_t dtype,
+                      void* stream);
+
+/*
+ * Causal linear attention with a decay for each head, from a state to a state:
+ * with g = exp(log_decay[h]),
+ *     S_t = g S_{t-1} + k_t v_t^T,    o_t = scale q_t S_t,    t = 1 .. n
+ * (S_0 = state_in or 0, state_out = S_n).  log_decay: (H) fp32 device memory, <=
+ * 0 (0: no decay, the sum of attn_linear_fwd; -inf: no memory).  Source:
+ * "Lightning Attention-2" (chatpaper.ai summary), the decay of its linear
+ * attention, and the chunk-wise form of "Gated Linear Attention Transformers
+ * with Hardware-Efficient Training" (nubint.ai review).
+ *
+ * q, k, v, o, dout, dq, dk, dv: (B, H, N, d) of one 16-bit type; states:
+ * (B, H, d, d) fp32, S[a][c] = feature a of k, feature c of v.  All device
+ * memory of the current device, 16-byte aligned (log_decay and lens 4-byte).
+ * lens: NULL, or (B) int32 tokens of each sequence (clamped to 0 .. N): rows
+ * past it are neither read into a result nor written; a sequence of length 0
+ * hands its state on unchanged.
+ *
+ * attn_decay_fwd: the chunked form, for whole prompts and training.  state_in
+ * and state_out may each be NULL and may be the same array.
+ *
+ * attn_decay_bwd: dq, dk, dv and dstate_in (may be NULL) for the gradients dout
+ * of o and dstate_out (NULL: 0) of state_out; the forward's outputs are not
+ * needed.  The decay is a constant of the head: no gradient of it.  dstate_in
+ * must not be one of the arrays read (ATTN_ERR_ARG).
+ *
+ * attn_decay_step: the recurrent form for one token, N = 1; state_out may be
+ * state_in.
+ *
+ * workspace: attn_decay_workspace_bytes() bytes, 16-byte aligned (NULL when that
+ * is 0); its contents on entry do not matter.  States are fp32 throughout;
+ * chunked products with a state or with in-chunk weights see them rounded to
+ * the input's 16-bit type.  Errors as attn_fwd.
+ */
+size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward);
+
+int attn_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                   const float* state_in, const int* lens, void* o, float* state_out,
+                   void* workspace, int B, int H, int N, int d, float scale, attn_dtype_t dtype,
+                   void* stream);
+
+int attn_decay_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                   const void* dout, const float* state_in, const float* dstate_out,
+                   const int* lens, void* dq, void* dk, void* dv, float* dstate_in,
+                   void* workspace, int B, int H, int N, int d, float scale, attn_dtype_t dtype,
+                   void* stream);
+
+int attn_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                    const float* state_in, void* o, float* state_out, int B, int H, int d,
+                    float scale, attn_dtype_t dtype, void* stream);
+
+/*
  * Backward that allocates nothing, for callers that cannot get device memory
  * for a workspace: for example a plugin inside a host framework that owns
  * every device allocation through its own pool and hands the plugin only the
@@ -308,7 +421,8 @@ int attn_sdpa_host(const void* q, const void* k, const void* v, const void* dout
 
 /*
  * Synchronises `stream`, then returns ATTN_OK, ATTN_ERR_TIMEOUT if a kernel
- * of this library recorded a wait that ran out since the last call, or
+ * of this library recorded a wait that ran out since the last call,
+ * ATTN_ERR_PAGE if one met a page index or a length outside the cache, or
  * ATTN_ERR_LAUNCH if the stream reported a CUDA error.  Clears the device
  * error word of the current device.
  */

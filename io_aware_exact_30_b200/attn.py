@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -23,7 +24,7 @@ _DTYPES = {torch.bfloat16: ATTN_BF16, torch.float16: ATTN_FP16}
 STATUS = {
     0: "ATTN_OK", -1: "ATTN_ERR_NULL", -2: "ATTN_ERR_SHAPE", -3: "ATTN_ERR_HEADDIM",
     -4: "ATTN_ERR_ALIGN", -5: "ATTN_ERR_DTYPE", -6: "ATTN_ERR_DEVICE", -7: "ATTN_ERR_LAUNCH",
-    -8: "ATTN_ERR_TIMEOUT", -9: "ATTN_ERR_ARG", -10: "ATTN_ERR_SCRATCH",
+    -8: "ATTN_ERR_TIMEOUT", -9: "ATTN_ERR_ARG", -10: "ATTN_ERR_SCRATCH", -11: "ATTN_ERR_PAGE",
 }
 
 # Kernel launches one attn_bwd call makes: the preprocess, then the main
@@ -36,6 +37,8 @@ EXPORTS = ("attn_fwd", "attn_bwd", "attn_bwd_prep", "attn_bwd_main", "attn_bwd_w
            "attn_bwd_noalloc", "attn_sdpa_host", "attn_sdpa_host_scratch_bytes",
            "attn_fwd_blocksparse", "attn_bwd_blocksparse", "attn_fp8_quantize", "attn_fwd_fp8",
            "attn_fwd_dropout", "attn_bwd_dropout", "attn_linear_fwd", "attn_linear_workspace_bytes",
+           "attn_cache_append", "attn_cache_attend", "attn_cache_attend_workspace_bytes",
+           "attn_decay_fwd", "attn_decay_bwd", "attn_decay_step", "attn_decay_workspace_bytes",
            "attn_last_device_status", "attn_selftest_wait_timeout",
            "attn_last_cuda_error_string", "attn_strerror", "attn_version")
 
@@ -81,6 +84,20 @@ def lib() -> ctypes.CDLL:
         L.attn_linear_workspace_bytes.restype = sz
         L.attn_linear_fwd.argtypes = [vp] * 5 + [ci, ci, ci, ci, cf, ci, vp]
         L.attn_linear_fwd.restype = ci
+        L.attn_cache_append.argtypes = [vp] * 9 + [ci] * 8 + [vp]
+        L.attn_cache_append.restype = ci
+        L.attn_cache_attend_workspace_bytes.argtypes = [ci] * 6
+        L.attn_cache_attend_workspace_bytes.restype = sz
+        L.attn_cache_attend.argtypes = [vp] * 11 + [ci] * 10 + [cf, ci, vp]
+        L.attn_cache_attend.restype = ci
+        L.attn_decay_workspace_bytes.argtypes = [ci] * 5
+        L.attn_decay_workspace_bytes.restype = sz
+        L.attn_decay_fwd.argtypes = [vp] * 9 + [ci] * 4 + [cf, ci, vp]
+        L.attn_decay_fwd.restype = ci
+        L.attn_decay_bwd.argtypes = [vp] * 13 + [ci] * 4 + [cf, ci, vp]
+        L.attn_decay_bwd.restype = ci
+        L.attn_decay_step.argtypes = [vp] * 7 + [ci] * 3 + [cf, ci, vp]
+        L.attn_decay_step.restype = ci
         u64 = ctypes.c_ulonglong
         L.attn_fwd_dropout.argtypes = [vp] * 5 + [ci, ci, ci, ci, ci, cf, cf, u64, ci, vp]
         L.attn_fwd_dropout.restype = ci
@@ -359,6 +376,176 @@ def attn_linear_fwd(q, k, v, o, workspace, scale: float | None = None, stream=No
     _check(rc, "attn_linear_fwd")
 
 
+# Page sizes (tokens) of the 8-bit cache.
+PAGE_SIZES = (16, 32, 64, 128)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+class Cache8(NamedTuple):
+    """A paged key/value cache in e4m3: codes (num_pages, Hkv, page, d)
+    float8_e4m3fn (or the same bytes as uint8), and one power-of-two fp32 scale for
+    each page and head, (num_pages, Hkv); value = code * scale."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def cache_alloc(num_pages: int, Hkv: int, page: int, d: int, device="cuda") -> Cache8:
+    """An empty cache.  Pages need no clearing when they are used again."""
+    if page not in PAGE_SIZES:
+        raise ValueError(f"page must be one of {PAGE_SIZES}")
+    codes = [torch.zeros((num_pages, Hkv, page, d), dtype=torch.uint8,
+                         device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.zeros((num_pages, Hkv), dtype=torch.float32, device=device) for _ in range(2)]
+    return Cache8(*codes, *scales)
+
+
+def _cache_shape(cache, d, page_table, B):
+    """(num_pages, Hkv, page, max_pages) of a cache whose arrays fit together."""
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.shape[3] != d or k.shape[2] not in PAGE_SIZES:
+        raise ValueError(f"cache codes must be (num_pages, Hkv, page, {d}), page one of {PAGE_SIZES}")
+    if k.dtype not in _CODES or v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("cache codes must be float8_e4m3fn or uint8, k and v alike")
+    P, Hkv, page = k.shape[:3]
+    for s in (ks, vs):
+        if s.dtype != torch.float32 or tuple(s.shape) != (P, Hkv) or not s.is_contiguous():
+            raise ValueError("cache scales must be contiguous float32 (num_pages, Hkv) tensors")
+    if not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("cache codes must be contiguous")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be a contiguous int32 ({B}, max_pages) tensor")
+    return P, Hkv, page, page_table.shape[1]
+
+
+def _check_lens(t, B, name):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 ({B},) tensor")
+
+
+def attn_cache_append(k, v, cache: Cache8, page_table, lens, n_new=None, stream=None) -> None:
+    """Stores the first n_new[b] (None: all T) new tokens of k, v (B, Hkv, T, d)
+    behind the lens[b] tokens that sequence b holds; lens is not updated."""
+    B, H, T, d = _shape(k)
+    _same(k, k, v, names=("k", "v"))
+    P, Hkv, page, width = _cache_shape(cache, d, page_table, B)
+    if H != Hkv:
+        raise ValueError(f"k and v have {H} heads, the cache {Hkv}")
+    _check_lens(lens, B, "lens")
+    _check_lens(n_new, B, "n_new")
+    rc = lib().attn_cache_append(_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(page_table), _ptr(lens),
+                                 _ptr(n_new), B, H, T, d, P, page, width, _dtype(k),
+                                 ctypes.c_void_p(_stream(k.device, stream)))
+    _check(rc, "attn_cache_append")
+
+
+def attn_cache_attend_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, d: int, max_len: int) -> int:
+    return int(lib().attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len))
+
+
+def attn_cache_attend(q, cache: Cache8, page_table, lens, o, lse, workspace=None, causal: bool = True,
+                      scale: float | None = None, q_lens=None, max_len: int | None = None,
+                      stream=None) -> None:
+    """O, LSE <- attention of the last q_lens[b] (None: T) queries of each sequence
+    over its lens[b] tokens in the cache; rows past q_lens[b] are left as they
+    were.  max_len: an upper bound of lens (None: the table's capacity)."""
+    B, Hq, T, d = _shape(q)
+    _same(q, q, o, names=("q", "o"))
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 (B, Hq, T) tensor")
+    P, Hkv, page, width = _cache_shape(cache, d, page_table, B)
+    _check_lens(lens, B, "lens")
+    _check_lens(q_lens, B, "q_lens")
+    max_len = width * page if max_len is None else int(max_len)
+    need = attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace needs {need} bytes")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    rc = lib().attn_cache_attend(_ptr(q), *map(_ptr, cache), _ptr(page_table), _ptr(lens), _ptr(q_lens),
+                                 _ptr(o), _ptr(lse), _ptr(workspace), B, Hq, Hkv, T, d, P, page,
+                                 width, max_len, int(bool(causal)), scale, _dtype(q),
+                                 ctypes.c_void_p(_stream(q.device, stream)))
+    _check(rc, "attn_cache_attend")
+
+
+def _check_state(t, q, name):
+    B, H, _, d = q.shape
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, H, d, d)
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 ({B}, {H}, {d}, {d}) tensor")
+
+
+def _check_decay(log_decay, H):
+    if log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (H,) or not log_decay.is_contiguous():
+        raise ValueError(f"log_decay must be a contiguous float32 ({H},) tensor")
+
+
+def attn_decay_workspace_bytes(B: int, H: int, N: int, d: int, backward: bool = False) -> int:
+    return int(lib().attn_decay_workspace_bytes(B, H, N, d, int(bool(backward))))
+
+
+def _check_workspace(workspace, need):
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace needs {need} bytes")
+
+
+def attn_decay_fwd(q, k, v, log_decay, o, state_in=None, state_out=None, lens=None, workspace=None,
+                   scale: float | None = None, stream=None) -> None:
+    """O, state_out <- linear attention with a decay for each head, from state_in
+    (None: zeros); rows of o past lens[b] are left as they were."""
+    B, H, N, d = _shape(q)
+    _same(q, q, k, v, o, names=("q", "k", "v", "o"))
+    _check_decay(log_decay, H)
+    _check_state(state_in, q, "state_in")
+    _check_state(state_out, q, "state_out")
+    _check_lens(lens, B, "lens")
+    _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d, False))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    rc = lib().attn_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_in), _ptr(lens),
+                              _ptr(o), _ptr(state_out), _ptr(workspace), B, H, N, d, scale, _dtype(q),
+                              ctypes.c_void_p(_stream(q.device, stream)))
+    _check(rc, "attn_decay_fwd")
+
+
+def attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state_in=None, dstate_out=None,
+                   dstate_in=None, lens=None, workspace=None, scale: float | None = None,
+                   stream=None) -> None:
+    """dQ, dK, dV, dstate_in <- gradients of sum(O * dout) + sum(state_out *
+    dstate_out); rows past lens[b] are left as they were."""
+    B, H, N, d = _shape(q)
+    _same(q, q, k, v, dout, dq, dk, dv, names=("q", "k", "v", "dout", "dq", "dk", "dv"))
+    _check_decay(log_decay, H)
+    for t, n in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
+        _check_state(t, q, n)
+    _check_lens(lens, B, "lens")
+    _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d, True))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    rc = lib().attn_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dout), _ptr(state_in),
+                              _ptr(dstate_out), _ptr(lens), _ptr(dq), _ptr(dk), _ptr(dv),
+                              _ptr(dstate_in), _ptr(workspace), B, H, N, d, scale, _dtype(q),
+                              ctypes.c_void_p(_stream(q.device, stream)))
+    _check(rc, "attn_decay_bwd")
+
+
+def attn_decay_step(q, k, v, log_decay, state_in, o, state_out, scale: float | None = None,
+                    stream=None) -> None:
+    """O, state_out <- one token, q, k, v, o (B, H, 1, d); state_out may be state_in."""
+    B, H, N, d = _shape(q)
+    if N != 1:
+        raise ValueError("a step takes one token: q must be (B, H, 1, d)")
+    _same(q, q, k, v, o, names=("q", "k", "v", "o"))
+    _check_decay(log_decay, H)
+    _check_state(state_in, q, "state_in")
+    _check_state(state_out, q, "state_out")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    rc = lib().attn_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_in), _ptr(o),
+                               _ptr(state_out), B, H, d, scale, _dtype(q),
+                               ctypes.c_void_p(_stream(q.device, stream)))
+    _check(rc, "attn_decay_step")
+
+
 def attn_sdpa_host_scratch_bytes(B: int, H: int, N: int, d: int, with_backward: bool,
                                  heads_per_chunk: int = 0) -> int:
     return int(lib().attn_sdpa_host_scratch_bytes(B, H, N, d, int(bool(with_backward)),
@@ -484,6 +671,63 @@ def linear_forward(q, k, v, scale: float | None = None):
                      device=q.device)
     attn_linear_fwd(q, k, v, o, ws, scale)
     return o
+
+
+def cache_append(k, v, cache: Cache8, page_table, lens, n_new=None) -> None:
+    """Stores new tokens in the cache: attn_cache_append."""
+    attn_cache_append(k, v, cache, page_table, lens, n_new)
+
+
+def cache_attend(q, cache: Cache8, page_table, lens, causal: bool = True, scale: float | None = None,
+                 q_lens=None, max_len: int | None = None):
+    """Allocates O, LSE and the workspace and runs attn_cache_attend; returns
+    (o, lse).  Rows past q_lens[b] are 0 and -inf."""
+    B, Hq, T, d = _shape(q)
+    o = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
+    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    if q_lens is not None:
+        lse.fill_(-math.inf)
+    cap = page_table.shape[1] * cache.k.shape[2] if max_len is None else int(max_len)
+    need = attn_cache_attend_workspace_bytes(B, Hq, cache.k.shape[1], T, d, cap)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    attn_cache_attend(q, cache, page_table, lens, o, lse, ws, causal, scale, q_lens, cap)
+    return o, lse
+
+
+def decay_forward(q, k, v, log_decay, scale: float | None = None, state=None, lens=None):
+    """Allocates O, the state and the workspace and runs attn_decay_fwd; returns
+    (o, state after the last token).  Rows past lens[b] are 0."""
+    B, H, N, d = _shape(q)
+    o = torch.empty_like(q) if lens is None else torch.zeros_like(q)
+    out = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+    need = attn_decay_workspace_bytes(B, H, N, d, False)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    attn_decay_fwd(q, k, v, log_decay, o, state, out, lens, ws, scale)
+    return o, out
+
+
+def decay_backward(q, k, v, log_decay, dout, scale: float | None = None, state=None, dstate=None,
+                   lens=None):
+    """Allocates the gradients and the workspace and runs attn_decay_bwd; returns
+    (dq, dk, dv, gradient of the state before the first token).  Rows past
+    lens[b] are 0."""
+    B, H, N, d = _shape(q)
+    new = torch.empty_like if lens is None else torch.zeros_like
+    dq, dk, dv = new(q), new(k), new(v)
+    ds = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+    need = attn_decay_workspace_bytes(B, H, N, d, True)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state, dstate, ds, lens, ws, scale)
+    return dq, dk, dv, ds
+
+
+def decay_step(q, k, v, log_decay, state, scale: float | None = None, state_out=None):
+    """One token: returns (o, state_out); state_out defaults to a new tensor and
+    may be ``state`` itself."""
+    o = torch.empty_like(q)
+    out = torch.empty_like(state) if state_out is None else state_out
+    attn_decay_step(q, k, v, log_decay, state, o, out, scale)
+    return o, out
 
 
 # ------------------------------------------------------------ several GPUs --

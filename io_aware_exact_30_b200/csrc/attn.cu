@@ -17,6 +17,8 @@
 #include "bwd128_sm100.cuh"
 #include "fp8_sm100.cuh"
 #include "linear_sm100.cuh"
+#include "cache8.cuh"
+#include "decay_sm100.cuh"
 
 namespace {
 
@@ -654,7 +656,7 @@ int attn_last_device_status(void* stream) {
     if (cudaMemcpyFromSymbol(&word, attn::g_attn_error, sizeof(int)) != cudaSuccess ||
         cudaMemcpyToSymbol(attn::g_attn_error, &zero, sizeof(int)) != cudaSuccess)
         return ATTN_ERR_LAUNCH;
-    return word == 0 ? ATTN_OK : ATTN_ERR_TIMEOUT;
+    return word == 0 ? ATTN_OK : (word == ATTN_ERR_PAGE ? ATTN_ERR_PAGE : ATTN_ERR_TIMEOUT);
 }
 
 int attn_selftest_wait_timeout(unsigned timeout_us, void* stream) {
@@ -680,6 +682,7 @@ const char* attn_strerror(int status) {
         case ATTN_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
         case ATTN_ERR_ARG: return "scale must be finite and > 0 (or a scalar argument is out of range)";
         case ATTN_ERR_SCRATCH: return "not enough scratch: the built-in array (attn_bwd_noalloc) or scratch_bytes (attn_sdpa_host) is too small";
+        case ATTN_ERR_PAGE: return "a page index or a length outside the cache";
         default: return "unknown status";
     }
 }
@@ -847,4 +850,236 @@ extern "C" int attn_sdpa_host(const void* q, const void* k, const void* v, const
         if (rc == ATTN_OK) rc = ATTN_ERR_LAUNCH;
     }
     return rc;
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit paged cache.
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_cache(int num_pages, int page, int max_pages, int Hkv) {
+    if (page != 16 && page != 32 && page != 64 && page != 128) return ATTN_ERR_ARG;
+    if (num_pages < 1 || max_pages < 1 || Hkv < 1) return ATTN_ERR_SHAPE;
+    // positions are 32-bit
+    if (1LL * max_pages * page >= (1LL << 31)) return ATTN_ERR_SHAPE;
+    return ATTN_OK;
+}
+
+template <int D, bool BF16>
+void launch_append(const attn::AppendParams& p, unsigned grid, cudaStream_t st) {
+    switch (p.page * D / 1024) {
+        case 1: attn::cache_append_kernel<D, BF16, 1><<<grid, 128, 0, st>>>(p); break;
+        case 2: attn::cache_append_kernel<D, BF16, 2><<<grid, 128, 0, st>>>(p); break;
+        case 4: attn::cache_append_kernel<D, BF16, 4><<<grid, 128, 0, st>>>(p); break;
+        case 8: attn::cache_append_kernel<D, BF16, 8><<<grid, 128, 0, st>>>(p); break;
+        default: attn::cache_append_kernel<D, BF16, D == 128 ? 16 : 8><<<grid, 128, 0, st>>>(p);
+    }
+}
+
+}  // namespace
+
+extern "C" int attn_cache_append(const void* k, const void* v, unsigned char* k8,
+                                 unsigned char* v8, float* k_scale, float* v_scale,
+                                 const int* page_table, const int* lens, const int* n_new, int B,
+                                 int Hkv, int T, int d, int num_pages, int page, int max_pages,
+                                 attn_dtype_t dtype, void* stream) {
+    if (!k || !v || !k8 || !v8 || !k_scale || !v_scale || !page_table || !lens)
+        return ATTN_ERR_NULL;
+    int rc = check_shape(B, Hkv, T, d, dtype, 1.f);
+    if (rc || (rc = check_cache(num_pages, page, max_pages, Hkv))) return rc;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || !aligned4(page_table) || !aligned4(lens) || !aligned4(n_new))
+        return ATTN_ERR_ALIGN;
+    if (k8 == v8 || k_scale == v_scale) return ATTN_ERR_ARG;
+    const int touched = (T + page - 2) / page + 1;
+    const long long grid = 2LL * B * Hkv * touched;
+    if (grid >= (1LL << 31)) return ATTN_ERR_SHAPE;
+    int dev;
+    if ((rc = check_device(&dev))) return rc;
+    const void* ptrs[] = {k, v, k8, v8, k_scale, v_scale, page_table, lens};
+    for (const void* ptr : ptrs)
+        if (!on_device(ptr, dev)) return ATTN_ERR_DEVICE;
+    if (n_new && !on_device(n_new, dev)) return ATTN_ERR_DEVICE;
+    attn::AppendParams p;
+    p.x[0] = static_cast<const uint8_t*>(k), p.x[1] = static_cast<const uint8_t*>(v);
+    p.codes[0] = k8, p.codes[1] = v8;
+    p.scale[0] = k_scale, p.scale[1] = v_scale;
+    p.table = page_table, p.lens = lens, p.n_new = n_new;
+    p.B = B, p.Hkv = Hkv, p.T = T, p.num_pages = num_pages, p.page = page, p.max_pages = max_pages;
+    p.touched = touched;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned g = static_cast<unsigned>(grid);
+    if (d == 64)
+        dtype == ATTN_BF16 ? launch_append<64, true>(p, g, st) : launch_append<64, false>(p, g, st);
+    else
+        dtype == ATTN_BF16 ? launch_append<128, true>(p, g, st) : launch_append<128, false>(p, g, st);
+    return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+namespace {
+int check_attend(int B, int Hq, int Hkv, int T, int d, int dtype, float scale) {
+    int rc = check_shape(B, Hq, T, d, dtype, scale);
+    if (rc) return rc;
+    return Hkv < 1 || Hq % Hkv ? ATTN_ERR_SHAPE : ATTN_OK;
+}
+}  // namespace
+
+extern "C" size_t attn_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int T, int d,
+                                                    int max_len) {
+    if (check_attend(B, Hq, Hkv, T, d, ATTN_BF16, 1.f) || max_len < 1) return 0;
+    return 0;
+}
+
+extern "C" int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned char* v8,
+                                 const float* k_scale, const float* v_scale, const int* page_table,
+                                 const int* lens, const int* q_lens, void* o, float* lse,
+                                 void* workspace, int B, int Hq, int Hkv, int T, int d,
+                                 int num_pages, int page, int max_pages, int max_len, int causal,
+                                 float scale, attn_dtype_t dtype, void* stream) {
+    if (!q || !k8 || !v8 || !k_scale || !v_scale || !page_table || !lens || !o || !lse)
+        return ATTN_ERR_NULL;
+    int rc = check_attend(B, Hq, Hkv, T, d, dtype, scale);
+    if (rc || (rc = check_cache(num_pages, page, max_pages, Hkv))) return rc;
+    if (max_len < 1) return ATTN_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k8) || !aligned16(v8) || !aligned16(o) || !aligned4(lse) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page_table) || !aligned4(lens) ||
+        !aligned4(q_lens) || !aligned16(workspace))
+        return ATTN_ERR_ALIGN;
+    int dev;
+    if ((rc = check_device(&dev))) return rc;
+    const void* ptrs[] = {q, k8, v8, k_scale, v_scale, page_table, lens, o, lse};
+    for (const void* ptr : ptrs)
+        if (!on_device(ptr, dev)) return ATTN_ERR_DEVICE;
+    if ((q_lens && !on_device(q_lens, dev)) || (workspace && !on_device(workspace, dev)))
+        return ATTN_ERR_DEVICE;
+    attn::AttendParams p;
+    p.q = static_cast<const uint8_t*>(q);
+    p.codes[0] = k8, p.codes[1] = v8;
+    p.scale[0] = k_scale, p.scale[1] = v_scale;
+    p.table = page_table, p.lens = lens, p.q_lens = q_lens;
+    p.o = static_cast<uint8_t*>(o), p.lse = lse;
+    p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T;
+    p.num_pages = num_pages, p.page = page, p.max_pages = max_pages;
+    p.causal = causal ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned g = static_cast<unsigned>((1LL * B * Hq * T + 3) / 4);
+    const bool bf = dtype == ATTN_BF16;
+    if (d == 64)
+        bf ? attn::cache_attend_rows_kernel<64, true><<<g, 128, 0, st>>>(p)
+           : attn::cache_attend_rows_kernel<64, false><<<g, 128, 0, st>>>(p);
+    else
+        bf ? attn::cache_attend_rows_kernel<128, true><<<g, 128, 0, st>>>(p)
+           : attn::cache_attend_rows_kernel<128, false><<<g, 128, 0, st>>>(p);
+    return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+// ---------------------------------------------------------------------------
+// Linear attention with a decay for each head.
+namespace {
+
+int check_decay(const void* const* required, int nr, const void* const* optional, int no, int B,
+                int H, int N, int d, int dtype, float scale, int* dev) {
+    for (int i = 0; i < nr; ++i)
+        if (!required[i]) return ATTN_ERR_NULL;
+    int rc = check_shape(B, H, N, d, dtype, scale);
+    if (rc) return rc;
+    // the states: B H d^2 fp32
+    if (1LL * B * H * d * d >= (1LL << 40)) return ATTN_ERR_SHAPE;
+    for (int i = 0; i < nr; ++i)
+        if (!aligned16(required[i])) return ATTN_ERR_ALIGN;
+    for (int i = 0; i < no; ++i)
+        if (!aligned16(optional[i])) return ATTN_ERR_ALIGN;
+    if ((rc = check_device(dev))) return rc;
+    for (int i = 0; i < nr; ++i)
+        if (!on_device(required[i], *dev)) return ATTN_ERR_DEVICE;
+    for (int i = 0; i < no; ++i)
+        if (optional[i] && !on_device(optional[i], *dev)) return ATTN_ERR_DEVICE;
+    return ATTN_OK;
+}
+
+int launch_decay(const attn::DecayParams& p, int passes, int d, int dtype, cudaStream_t st) {
+    const dim3 g(static_cast<unsigned>(p.B * p.H), static_cast<unsigned>(passes));
+    const bool bf = dtype == ATTN_BF16;
+    if (d == 64)
+        bf ? attn::decay_recurrent_kernel<64, true><<<g, 64, 0, st>>>(p)
+           : attn::decay_recurrent_kernel<64, false><<<g, 64, 0, st>>>(p);
+    else
+        bf ? attn::decay_recurrent_kernel<128, true><<<g, 128, 0, st>>>(p)
+           : attn::decay_recurrent_kernel<128, false><<<g, 128, 0, st>>>(p);
+    return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward) {
+    (void)backward;
+    if (check_shape(B, H, N, d, ATTN_BF16, 1.f)) return 0;
+    return 0;
+}
+
+extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* state_in, const int* lens, void* o, float* state_out,
+                              void* workspace, int B, int H, int N, int d, float scale,
+                              attn_dtype_t dtype, void* stream) {
+    const void* req[] = {q, k, v, o};
+    const void* opt[] = {state_in, state_out, workspace};
+    if (!log_decay) return ATTN_ERR_NULL;
+    if (!aligned4(log_decay) || !aligned4(lens)) return ATTN_ERR_ALIGN;
+    int dev;
+    int rc = check_decay(req, 4, opt, 3, B, H, N, d, dtype, scale, &dev);
+    if (rc) return rc;
+    if (!on_device(log_decay, dev) || (lens && !on_device(lens, dev))) return ATTN_ERR_DEVICE;
+    attn::DecayParams p{};
+    p.pass[0] = {q, k, v, o, state_in, state_out, 0, 0};
+    p.log_decay = log_decay, p.lens = lens;
+    p.B = B, p.H = H, p.N = N, p.scale = scale;
+    return launch_decay(p, 1, d, dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              const void* dout, const float* state_in, const float* dstate_out,
+                              const int* lens, void* dq, void* dk, void* dv, float* dstate_in,
+                              void* workspace, int B, int H, int N, int d, float scale,
+                              attn_dtype_t dtype, void* stream) {
+    const void* req[] = {q, k, v, dout, dq, dk, dv};
+    const void* opt[] = {state_in, dstate_out, dstate_in, workspace};
+    if (!log_decay) return ATTN_ERR_NULL;
+    if (!aligned4(log_decay) || !aligned4(lens)) return ATTN_ERR_ALIGN;
+    if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in)) return ATTN_ERR_ARG;
+    int dev;
+    int rc = check_decay(req, 7, opt, 4, B, H, N, d, dtype, scale, &dev);
+    if (rc) return rc;
+    if (!on_device(log_decay, dev) || (lens && !on_device(lens, dev))) return ATTN_ERR_DEVICE;
+    attn::DecayParams p{};
+    p.pass[0] = {dout, v, k, dq, state_in, nullptr, 1, 0};
+    p.pass[1] = {v, dout, q, dk, dstate_out, nullptr, 1, 1};
+    p.pass[2] = {k, q, dout, dv, dstate_out, dstate_in, 0, 1};
+    p.log_decay = log_decay, p.lens = lens;
+    p.B = B, p.H = H, p.N = N, p.scale = scale;
+    return launch_decay(p, 3, d, dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int attn_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                               const float* state_in, void* o, float* state_out, int B, int H,
+                               int d, float scale, attn_dtype_t dtype, void* stream) {
+    const void* req[] = {q, k, v, state_in, o, state_out};
+    if (!log_decay) return ATTN_ERR_NULL;
+    if (!aligned4(log_decay)) return ATTN_ERR_ALIGN;
+    int dev;
+    int rc = check_decay(req, 6, nullptr, 0, B, H, 1, d, dtype, scale, &dev);
+    if (rc) return rc;
+    if (!on_device(log_decay, dev)) return ATTN_ERR_DEVICE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned g = static_cast<unsigned>(B * H);
+    const bool bf = dtype == ATTN_BF16;
+#define STEP_LAUNCH(D_, BF_) \
+    attn::decay_step_kernel<D_, BF_><<<g, D_, 0, st>>>(q, k, v, log_decay, state_in, state_out, o, H, scale)
+    if (d == 64)
+        bf ? STEP_LAUNCH(64, true) : STEP_LAUNCH(64, false);
+    else
+        bf ? STEP_LAUNCH(128, true) : STEP_LAUNCH(128, false);
+#undef STEP_LAUNCH
+    return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
