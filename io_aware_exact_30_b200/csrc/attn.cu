@@ -129,6 +129,8 @@ int check_device(int* dev_out) {
     ok &= cudaFuncSetAttribute(attn::linear_fused_kernel<false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                attn::LinFusedCfg::SMEM_BYTES) == cudaSuccess;
+    ok &= attn::decay_set_attributes<64, true>() && attn::decay_set_attributes<64, false>() &&
+          attn::decay_set_attributes<128, true>() && attn::decay_set_attributes<128, false>();
     ok &= attn::bwd_set_attributes();
     ok &= attn::bwd128_set_attributes();
     if (!ok) {
@@ -999,24 +1001,30 @@ int check_decay(const void* const* required, int nr, const void* const* optional
     return ATTN_OK;
 }
 
-int launch_decay(const attn::DecayParams& p, int passes, int d, int dtype, cudaStream_t st) {
-    const dim3 g(static_cast<unsigned>(p.B * p.H), static_cast<unsigned>(passes));
+int launch_decay(const void* const* tensors, int nt, attn::DecayParams& p, int d, int dtype,
+                 void* workspace, cudaStream_t st) {
+    const int BH = p.B * p.H;
+    attn::DecayMaps maps;
+    for (int i = 0; i < 4; ++i)
+        if (!make_map(&maps.m[i], tensors[i < nt ? i : 0], dtype, BH, p.N, d)) return ATTN_ERR_LAUNCH;
+    attn::decay_segments(p.B, p.H, p.N, d, p.passes, &p.nseg, &p.seg_chunks);
+    if (p.nseg > 1 && !workspace) return ATTN_ERR_NULL;
+    if (1LL * BH * (d / 64) * p.passes * p.nseg >= (1LL << 31) || BH > 65535 * (p.nseg > 1 ? 1 : 32768))
+        return ATTN_ERR_SHAPE;
+    p.seg = static_cast<float*>(workspace);
     const bool bf = dtype == ATTN_BF16;
     if (d == 64)
-        bf ? attn::decay_recurrent_kernel<64, true><<<g, 64, 0, st>>>(p)
-           : attn::decay_recurrent_kernel<64, false><<<g, 64, 0, st>>>(p);
+        bf ? attn::decay_launch<64, true>(maps, p, st) : attn::decay_launch<64, false>(maps, p, st);
     else
-        bf ? attn::decay_recurrent_kernel<128, true><<<g, 128, 0, st>>>(p)
-           : attn::decay_recurrent_kernel<128, false><<<g, 128, 0, st>>>(p);
+        bf ? attn::decay_launch<128, true>(maps, p, st) : attn::decay_launch<128, false>(maps, p, st);
     return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
 
 extern "C" size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward) {
-    (void)backward;
     if (check_shape(B, H, N, d, ATTN_BF16, 1.f)) return 0;
-    return 0;
+    return attn::decay_workspace(B, H, N, d, backward ? 3 : 1);
 }
 
 extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -1032,10 +1040,10 @@ extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const
     if (rc) return rc;
     if (!on_device(log_decay, dev) || (lens && !on_device(lens, dev))) return ATTN_ERR_DEVICE;
     attn::DecayParams p{};
-    p.pass[0] = {q, k, v, o, state_in, state_out, 0, 0};
+    p.pass[0] = {0, 1, 2, o, state_in, state_out, 0, 0};
     p.log_decay = log_decay, p.lens = lens;
-    p.B = B, p.H = H, p.N = N, p.scale = scale;
-    return launch_decay(p, 1, d, dtype, static_cast<cudaStream_t>(stream));
+    p.passes = 1, p.B = B, p.H = H, p.N = N, p.scale = scale;
+    return launch_decay(req, 3, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -1053,12 +1061,13 @@ extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const
     if (rc) return rc;
     if (!on_device(log_decay, dev) || (lens && !on_device(lens, dev))) return ATTN_ERR_DEVICE;
     attn::DecayParams p{};
-    p.pass[0] = {dout, v, k, dq, state_in, nullptr, 1, 0};
-    p.pass[1] = {v, dout, q, dk, dstate_out, nullptr, 1, 1};
-    p.pass[2] = {k, q, dout, dv, dstate_out, dstate_in, 0, 1};
+    // tensors 0 q, 1 k, 2 v, 3 dout
+    p.pass[0] = {3, 2, 1, dq, state_in, nullptr, 1, 0};
+    p.pass[1] = {2, 3, 0, dk, dstate_out, nullptr, 1, 1};
+    p.pass[2] = {1, 0, 3, dv, dstate_out, dstate_in, 0, 1};
     p.log_decay = log_decay, p.lens = lens;
-    p.B = B, p.H = H, p.N = N, p.scale = scale;
-    return launch_decay(p, 3, d, dtype, static_cast<cudaStream_t>(stream));
+    p.passes = 3, p.B = B, p.H = H, p.N = N, p.scale = scale;
+    return launch_decay(req, 4, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int attn_decay_step(const void* q, const void* k, const void* v, const float* log_decay,

@@ -20,10 +20,8 @@ namespace attn {
 
 // One pass of the operator over x_t (in place of q), y_t (k) and z_t (v).
 struct DecayPass {
-    const void* x;
-    const void* y;
-    const void* z;
-    void* out;
+    int x, y, z;         // which of the tensor maps
+    void* out;           // (B, H, N, D)
     const float* init;   // (B, H, D, D) or null: the state before the first token
     float* last;         // (B, H, D, D) or null: the state after the last token
     int transposed;      // init is stored transposed
@@ -34,8 +32,14 @@ struct DecayParams {
     DecayPass pass[3];
     const float* log_decay;  // (H)
     const int* lens;         // (B) or null
-    int B, H, N;
+    float* seg;              // (passes, nseg, B H, D, D): states of the segments
+    int passes, B, H, N;
+    int nseg, seg_chunks;    // a sequence's chunks in segments of seg_chunks
     float scale;
+};
+
+struct DecayMaps {
+    CUtensorMap m[4];
 };
 
 __device__ __forceinline__ int decay_len(const int* lens, int b, int N) {
@@ -50,49 +54,551 @@ __device__ __forceinline__ float decay_log(const float* log_decay, int h) {
     return fmaxf(log_decay[h], -1e4f);
 }
 
-// Token by token: one CTA per (pass, head), thread = column of the state.
+constexpr int kDecayChunk = 128;
+
+// Tokens of segment `seg` of a sequence of n: chunks [c0, c1).
+__device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* c0, int* c1) {
+    const int all = (n + kDecayChunk - 1) / kDecayChunk;
+    *c0 = min(seg * seg_chunks, all);
+    *c1 = min(*c0 + seg_chunks, all);
+}
+
+// The chunked form.  One CTA per (pass, head, 64 value features, segment) walks
+// its chunks of 128 tokens with the state in registers.  With L the decay and,
+// for a chunk of n tokens in their order of walking, pos = 0 .. n - 1:
+//   A    = X Y^T                              tensor memory
+//   P_ij = scale A_ij L^(pos_i - pos_j)       pos_j <= pos_i, 16-bit
+//   OX   = X S                                S: 16-bit copy of the state
+//   O_i  = L^(pos_i + 1) OX_i + (P Z)_i
+//   S   <- L^n S + Y^T Zh,   Zh_j = L^(n - 1 - pos_j) Z_j
+// Backwards (a gradient G for S) the token's own term enters before the decay:
+// OX_i is weighted with L^pos_i and Zh_j with scale L^(n - pos_j).
+//
+// The state is an fp32 result of its own, so Zh must not be rounded to the
+// 16-bit type: it goes to the tensor cores as two (fp16, 22 bits) or three (bf16,
+// 24 bits) 16-bit pieces, side by side in the N extent of one product with Y,
+// and the pieces' sums are added in fp32.  (One bf16 piece put 2e-3 on the state,
+// two 3e-6, three 2e-7, the fp32 sums' own.)  P, the copy of S that X meets and the
+// result are rounded to the 16-bit type, half a step each: they only reach the
+// 16-bit result.
+//
+// Bound by the tensor pipe and its hand-overs at D = 128 (per chunk A 512, Y^T Zh
+// 768, X S and P Z 380 cycles each against 1300 for the chunk's share of HBM
+// bandwidth), by HBM at D = 64.
+//
+// Roles (448 threads): warp 0 loads (TMA), warp 1 issues the products, warps 2-9
+// make P and the output (thread = token; warps 2-5 keys 0-63 of P and features
+// 0-31, warps 6-9 the rest), warps 10-13 hold the state (thread = feature of y)
+// and make Zh (thread = token).  Issue order: A_0, then per chunk Y^T Zh, X S,
+// A of the next chunk, P Z: while the row warps read X S and hand over P, the
+// next A runs, and the next P is made during P Z and Y^T Zh.  X, Y and Z have
+// their own barriers per stage, so each is reloaded as soon as its last product
+// is done (one barrier for the three left the loads too little time).
+//
+// STATE: only the segment's own contribution to the state (from zero).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(D) decay_recurrent_kernel(const DecayParams p) {
-    __shared__ float sx[D], sy[D];
-    const int bh = blockIdx.x, h = bh % p.H, b = bh / p.H, c = threadIdx.x;
-    const DecayPass& ps = p.pass[blockIdx.y];
-    const int n = decay_len(p.lens, b, p.N);
-    const float g = expf(decay_log(p.log_decay, h));
-    const size_t state = static_cast<size_t>(bh) * D * D;
-    // backwards the state is a gradient: scale enters with each token's term
-    // instead of with the result, and the decay follows the token
-    const float in = ps.reverse ? p.scale : 1.f, out = ps.reverse ? 1.f : p.scale;
-    float S[D];
-#pragma unroll
-    for (int a = 0; a < D; ++a)
-        S[a] = ps.init ? ps.init[state + (ps.transposed ? c * D + a : a * D + c)] : 0.f;
-    auto at = [&](const void* m, int t) {
-        const uint16_t v = static_cast<const uint16_t*>(m)[(static_cast<size_t>(bh) * p.N + t) * D + c];
-        const float2 f = unpack2<BF16>(v);
-        return f.x;
-    };
-    for (int i = 0; i < n; ++i) {
-        const int t = ps.reverse ? n - 1 - i : i;
-        __syncthreads();
-        sx[c] = at(ps.x, t);
-        sy[c] = at(ps.y, t);
-        const float z = at(ps.z, t) * in;
-        __syncthreads();
-        float o = 0.f;
-#pragma unroll
-        for (int a = 0; a < D; ++a) {
-            const float s = (ps.reverse ? S[a] : g * S[a]) + sy[a] * z;
-            o += sx[a] * s;
-            S[a] = ps.reverse ? g * s : s;
+struct DecayCfg {
+    static constexpr int NP = BF16 ? 3 : 2;             // pieces of Zh
+    static constexpr uint32_t XB = D * 256u;            // X of a chunk
+    static constexpr uint32_t YB = 32768u;              // Y; at D = 64 its upper half stays zero
+    static constexpr uint32_t ZB = 16384u;              // 64 features of Z
+    static constexpr uint32_t STAGE = XB + YB + ZB;
+    static constexpr uint32_t OFF_ZH = 2 * STAGE;
+    static constexpr uint32_t OFF_S = OFF_ZH + NP * ZB;  // D rows of 64 features
+    static constexpr uint32_t OFF_PW = OFF_S + D * 128u; // L^0 .. L^128, then L^31 .. L^0
+    static constexpr uint32_t OFF_BAR = OFF_PW + (132 + 32) * 4;
+    static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_XE = 6, B_YE = 8, B_ZE = 10, B_AF = 12,
+                         B_PF = 14, B_ZH = 15, B_KVF = 16, B_KVE = 17, B_SSF = 18, B_QSD = 19,
+                         B_OD = 20, B_OE = 21, B_DR = 22, NBAR = 23;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;
+    static constexpr uint32_t COL_KV = 256, COL_O = 448;  // tensor memory: A at 0 and 128
+    static constexpr int NROW = 256, NSTATE = 128, NTHREADS = 448;
+    static_assert(SMEM_BYTES <= 232448u, "dynamic shared memory above the sm_100 per-block limit");
+};
+
+template <int D, bool BF16, bool STATE>
+__global__ void __launch_bounds__(448, 1)
+    decay_chunk_kernel(const __grid_constant__ DecayMaps maps, const __grid_constant__ DecayParams p) {
+    using C = DecayCfg<D, BF16>;
+    constexpr int HALVES = D / 64, NP = C::NP;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // halves of a head next to each other, then the passes of a head: what they
+    // share is read while it is in L2
+    int id = blockIdx.x;
+    const int hf = id % HALVES;
+    id /= HALVES;
+    const int pi = id % p.passes;
+    id /= p.passes;
+    const int bh = id % (p.B * p.H), seg = id / (p.B * p.H);
+    const DecayPass& ps = p.pass[pi];
+    const bool rev = ps.reverse != 0;
+    const int len = decay_len(p.lens, bh / p.H, p.N);
+    int c0, c1;
+    decay_span(len, seg, p.seg_chunks, &c0, &c1);
+    const int nch = c1 - c0;
+    // chunk of step i, and its number of tokens
+    auto chunk = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
+    auto tokens = [&](int i) { return min(kDecayChunk, len - chunk(i) * kDecayChunk); };
+    const uint32_t bar0 = base + C::OFF_BAR;
+#define DBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + C::OFF_MISC);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    float* pw = reinterpret_cast<float*>(gbase + C::OFF_PW);
+    const double ld = decay_log(p.log_decay, bh % p.H);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NBAR; ++i) {
+            const int rows = i == C::B_PF || i == C::B_OE;
+            const int state = i == C::B_ZH || i == C::B_KVE || i == C::B_SSF;
+            mbar_init(DBAR(i), rows ? C::NROW : (state ? C::NSTATE : 1));
         }
-        static_cast<uint16_t*>(ps.out)[(static_cast<size_t>(bh) * p.N + t) * D + c] =
-            static_cast<uint16_t>(pack2<BF16>(o * out, 0.f));
+        *abort_flag = 0u;
+        fence_mbar_init();
     }
-    if (ps.last) {
+    // L^m by the exponential of a double product: a power's error stays one rounding
+    for (int m = threadIdx.x; m <= kDecayChunk; m += C::NTHREADS) {
+        pw[m] = static_cast<float>(exp(ld * m));
+        if (m < 32) pw[132 + 31 - m] = pw[m];
+    }
+    if (D == 64) {  // features 64-127 of Y: zeros that no load touches
+        for (int i = threadIdx.x; i < 2 * 1024; i += C::NTHREADS)
+            *reinterpret_cast<uint4*>(gbase + (i >> 10) * C::STAGE + C::XB + 16384u + (i & 1023) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(base + C::OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const CUtensorMap *mx = &maps.m[ps.x], *my = &maps.m[ps.y], *mz = &maps.m[ps.z];
+            bool ok = true;
+            int issued = 0;
+            for (int i = 0; i < nch; ++i) {
+                const int s = i & 1, row = chunk(i) * kDecayChunk;
+                const uint32_t par = ((i >> 1) - 1) & 1;
+                const uint32_t sx = base + s * C::STAGE, sy = sx + C::XB, sz = sy + C::YB;
+                if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_YE + s), par, abort_flag))) break;
+                mbar_arrive_expect_tx(DBAR(C::B_YF + s), D * 256u);
 #pragma unroll
-        for (int a = 0; a < D; ++a)
-            ps.last[state + a * D + c] = S[a];
+                for (int kb = 0; kb < HALVES; ++kb)
+                    tma_load_3d(sy + kb * 16384u, my, DBAR(C::B_YF + s), kb * 64, row, bh);
+                issued = 3 * i + 1;
+                if constexpr (!STATE) {
+                    if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_XE + s), par, abort_flag))) break;
+                    mbar_arrive_expect_tx(DBAR(C::B_XF + s), D * 256u);
+#pragma unroll
+                    for (int kb = 0; kb < HALVES; ++kb)
+                        tma_load_3d(sx + kb * 16384u, mx, DBAR(C::B_XF + s), kb * 64, row, bh);
+                }
+                issued = 3 * i + 2;
+                if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_ZE + s), par, abort_flag))) break;
+                mbar_arrive_expect_tx(DBAR(C::B_ZF + s), C::ZB);
+                tma_load_3d(sz, mz, DBAR(C::B_ZF + s), hf * 64, row, bh);
+                issued = 3 * i + 3;
+            }
+            if (!ok) {  // let the copies in flight land before the CTA exits
+                for (int k = issued > 6 ? issued - 6 : 0; k < issued; ++k) {
+                    const int i = k / 3, what = k % 3;
+                    if (STATE && what == 1) continue;
+                    const int b = what == 0 ? C::B_YF : (what == 1 ? C::B_XF : C::B_ZF);
+                    wait_drain(DBAR(b + (i & 1)), (i >> 1) & 1);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t ID_A = idesc_f16(BF16, 128, 128, false, false);     // X Y^T
+            constexpr uint32_t ID_KV = idesc_f16(BF16, 128, 64 * NP, true, true);  // Y^T Zh
+            constexpr uint32_t ID_O = idesc_f16(BF16, 128, 64, false, true);       // X S, P Z
+            // A of step i into its buffer, last read by the P Z of step i - 2; in
+            // a chunk that is not full, the rows past its end are cleared first
+            auto issue_a = [&](int i) -> bool {
+                const int s = i & 1;
+                if (!wait3(DBAR(C::B_XF + s), (i >> 1) & 1, true, DBAR(C::B_YF + s), (i >> 1) & 1, true,
+                           DBAR(C::B_OD), i & 1, i >= 2, abort_flag))
+                    return false;
+                if (tokens(i) < kDecayChunk && !wait_bounded(DBAR(C::B_ZH), i & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t sx = base + s * C::STAGE, sy = sx + C::XB;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
+                    mma_ss(tmem + 128u * s, sdesc_sw128(sx + off, 16, 1024), sdesc_sw128(sy + off, 16, 1024),
+                           ID_A, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(DBAR(C::B_AF + s));
+                return true;
+            };
+            bool ok = true;
+            if constexpr (!STATE) ok = nch == 0 || issue_a(0);
+            for (int i = 0; ok && i < nch; ++i) {
+                const int s = i & 1;
+                const uint32_t sx = base + s * C::STAGE, sy = sx + C::XB, sz = sy + C::YB;
+                // Zh written, the previous sums read by the state warps
+                if (!(ok = wait3(DBAR(C::B_ZH), i & 1, true, DBAR(C::B_KVE), (i - 1) & 1, i >= 1,
+                                 DBAR(C::B_YF + s), (i >> 1) & 1, STATE, abort_flag)))
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)  // 16 tokens (2048 bytes) per step
+                    mma_ss(tmem + C::COL_KV, sdesc_sw128(sy + kk * 2048u, 16384, 1024),
+                           sdesc_sw128(base + C::OFF_ZH + kk * 2048u, 16384, 1024), ID_KV, kk > 0 ? 1u : 0u);
+                mma_commit(DBAR(C::B_KVF));
+                mma_commit(DBAR(C::B_YE + s));
+                if constexpr (STATE) {
+                    mma_commit(DBAR(C::B_ZE + s));
+                } else {
+                    // the state's copy stored, the previous output read
+                    if (!(ok = wait3(DBAR(C::B_SSF), i & 1, true, DBAR(C::B_OE), (i - 1) & 1, i >= 1, 0u, 0u,
+                                     false, abort_flag)))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
+                        mma_ss(tmem + C::COL_O, sdesc_sw128(sx + off, 16, 1024),
+                               sdesc_sw128(base + C::OFF_S + kk * 2048u, 16384, 1024), ID_O, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(DBAR(C::B_QSD));
+                    mma_commit(DBAR(C::B_XE + s));
+                    if (i + 1 < nch && !(ok = issue_a(i + 1))) break;
+                    // P written and X S read: P Z takes its columns
+                    if (!(ok = wait_bounded(DBAR(C::B_PF), i & 1, abort_flag))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + C::COL_O, tmem + 128u * s + kk * 8u + (kk >> 2) * 32u,
+                               sdesc_sw128(sz + kk * 2048u, 16384, 1024), ID_O, kk > 0 ? 1u : 0u);
+                    mma_commit(DBAR(C::B_OD));
+                    mma_commit(DBAR(C::B_ZE + s));
+                }
+            }
+            if (!ok) {  // every issued MMA must finish before tensor memory is freed
+                mma_commit(DBAR(C::B_DR));
+                wait_drain(DBAR(C::B_DR), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 10) {
+        // ----------------------------------------- P and the output (rows)
+        const int hc = (warp - 2) >> 2;        // keys 64 hc.. of P, features 32 hc.. of O
+        const int wq = warp & 3, r = wq * 32 + lane;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const float* near = rev ? pw : pw + 132;
+        for (int i = 0; !STATE && i < nch; ++i) {
+            const int b = i & 1, n = tokens(i);
+            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_AF + b), (i >> 1) & 1, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t col = 128u * b + 64u * hc;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                const int cb = hc * 2 + cc;  // 32 keys: all before, all behind or around the row's warp
+                uint32_t pk[16];
+                if (rev ? cb < wq : cb > wq) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                    // the lower block is read before P is packed over it
+                } else {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + col + cc * 32u, v);
+                    tmem_ld_wait();
+                    reg_fence32(v);
+                    if (cb == wq) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int gap = rev ? e - lane : lane - e;
+                            v[e] = gap >= 0 ? __float_as_uint(__uint_as_float(v[e]) * (pw[gap] * p.scale)) : 0u;
+                        }
+                    } else {
+                        // L^(distance) as L^(from the row to the block's near end) times
+                        // L^(from there to the key), neither above 1
+                        const float u = p.scale * (rev ? pw[cb * 32 - r] : pw[r - cb * 32 - 31]);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * (u * near[e]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = pack2<BF16>(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                }
+                tmem_st16(lane_addr + col + cc * 16u, pk);  // over columns already read
+            }
+            tmem_st_wait();
+            // X S, weighted, before P Z takes its columns
+            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD), i & 1, abort_flag))) break;
+            tc_fence_after();
+            uint32_t ox[32];
+            tmem_ld32(lane_addr + C::COL_O + 32u * hc, ox);
+            tmem_ld_wait();
+            reg_fence32(ox);
+            tc_fence_before();
+            mbar_arrive(DBAR(C::B_PF));
+            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OD), i & 1, abort_flag))) break;
+            tc_fence_after();
+            uint32_t v[32];
+            tmem_ld32(lane_addr + C::COL_O + 32u * hc, v);
+            tmem_ld_wait();
+            reg_fence32(v);
+            tc_fence_before();
+            mbar_arrive(DBAR(C::B_OE));
+            if (r < n) {
+                const float w = rev ? pw[n - 1 - r] : pw[r + 1];
+                uint32_t o16[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
+                                         fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
+                uint4* dst = reinterpret_cast<uint4*>(
+                    static_cast<uint8_t*>(ps.out) +
+                    (static_cast<size_t>(bh) * p.N + chunk(i) * kDecayChunk + r) * (D * 2) + hf * 128 + hc * 64);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    dst[e] = make_uint4(o16[4 * e], o16[4 * e + 1], o16[4 * e + 2], o16[4 * e + 3]);
+            }
+        }
+    } else {
+        // ------------------------------------------------- the state and Zh
+        const int a = (warp & 3) * 32 + lane;  // feature of y == TMEM lane; token of Zh
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const size_t mat = static_cast<size_t>(bh) * D * D;
+        const size_t seg_mat = (static_cast<size_t>(pi) * p.nseg + seg) * p.B * p.H * D * D + mat;
+        const float zscale = rev ? p.scale : 1.f, copy = rev ? 1.f : p.scale;
+        float st[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) st[c] = 0.f;
+        if (!STATE && a < D) {
+            if (p.nseg > 1) {
+                const float4* src = reinterpret_cast<const float4*>(p.seg + seg_mat + a * D + hf * 64);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float4 f = src[c];
+                    st[4 * c] = f.x, st[4 * c + 1] = f.y, st[4 * c + 2] = f.z, st[4 * c + 3] = f.w;
+                }
+            } else if (ps.init && ps.transposed) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) st[c] = ps.init[mat + (hf * 64 + c) * D + a];
+            } else if (ps.init) {
+                const float4* src = reinterpret_cast<const float4*>(ps.init + mat + a * D + hf * 64);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float4 f = src[c];
+                    st[4 * c] = f.x, st[4 * c + 1] = f.y, st[4 * c + 2] = f.z, st[4 * c + 3] = f.w;
+                }
+            }
+        }
+        // row a of the state's 16-bit copy: eight 16-byte pieces placed by the
+        // 128-byte swizzle (piece j at j ^ (a mod 8))
+        auto store_copy = [&]() {
+            if (a < D) {
+                uint8_t* srow = gbase + C::OFF_S + a * 128;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(srow + ((j ^ (a & 7)) << 4)) =
+                        make_uint4(pack2<BF16>(st[8 * j] * copy, st[8 * j + 1] * copy),
+                                   pack2<BF16>(st[8 * j + 2] * copy, st[8 * j + 3] * copy),
+                                   pack2<BF16>(st[8 * j + 4] * copy, st[8 * j + 5] * copy),
+                                   pack2<BF16>(st[8 * j + 6] * copy, st[8 * j + 7] * copy));
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(DBAR(C::B_SSF));
+        };
+        // the sums of step i (complete) into the state: S <- L^n S + sums, L^n as a
+        // pair of floats so that its error does not add up over the chunks
+        const double full = exp(ld * kDecayChunk);
+        auto add_sums = [&](int i) {
+            tc_fence_after();
+            const double gd = tokens(i) == kDecayChunk ? full : exp(ld * tokens(i));
+            const float g = static_cast<float>(gd), g2 = static_cast<float>(gd - g);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                uint32_t v[32];
+                float sum[32];
+#pragma unroll
+                for (int k = NP - 1; k >= 0; --k) {  // the small pieces first
+                    tmem_ld32(lane_addr + C::COL_KV + 64u * k + 32u * cc, v);
+                    tmem_ld_wait();
+                    reg_fence32(v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        sum[e] = k == NP - 1 ? __uint_as_float(v[e]) : sum[e] + __uint_as_float(v[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    st[cc * 32 + e] = fmaf(g, st[cc * 32 + e], fmaf(g2, st[cc * 32 + e], sum[e]));
+            }
+            tc_fence_before();
+            mbar_arrive(DBAR(C::B_KVE));
+        };
+        if constexpr (!STATE) store_copy();
+        bool ok = true;
+        for (int i = 0; i < nch; ++i) {
+            const int s = i & 1, n = tokens(i);
+            // Z landed; the previous product has read Zh
+            ok = wait_bounded(DBAR(C::B_ZF + s), (i >> 1) & 1, abort_flag) &&
+                 (i == 0 || wait_bounded(DBAR(C::B_KVF), (i - 1) & 1, abort_flag));
+            if (n < kDecayChunk)  // Y is cleared below
+                ok = ok && wait_bounded(DBAR(C::B_YF + s), (i >> 1) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            uint8_t* zrow = gbase + s * C::STAGE + C::XB + C::YB + a * 128;
+            uint8_t* hrow = gbase + C::OFF_ZH + a * 128;
+            if (a < n) {
+                const float w = (rev ? pw[a + 1] : pw[n - 1 - a]) * zscale;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t at = (j ^ (a & 7)) << 4;
+                    const uint4 in = *reinterpret_cast<const uint4*>(zrow + at);
+                    const uint32_t z[4] = {in.x, in.y, in.z, in.w};
+                    uint32_t out[NP][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = unpack2<BF16>(z[e]);
+                        f.x *= w, f.y *= w;
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) {
+                            out[k][e] = pack2<BF16>(f.x, f.y);
+                            const float2 g = unpack2<BF16>(out[k][e]);
+                            f.x -= g.x, f.y -= g.y;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < NP; ++k)
+                        *reinterpret_cast<uint4*>(hrow + k * C::ZB + at) =
+                            make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+                }
+            } else {
+                // a token past the end: it may hold anything, NaN included, in y and z
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    *reinterpret_cast<uint4*>(zrow + j * 16) = none;
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4*>(hrow + k * C::ZB + j * 16) = none;
+#pragma unroll
+                    for (int k = 0; k < HALVES; ++k)
+                        *reinterpret_cast<uint4*>(gbase + s * C::STAGE + C::XB + k * 16384u + a * 128 + j * 16) =
+                            none;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(DBAR(C::B_ZH));
+            if (i >= 1) {
+                add_sums(i - 1);
+                if constexpr (!STATE) {
+                    // the copy was last read by X S of step i - 1
+                    ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD), (i - 1) & 1, abort_flag));
+                    if (!ok) break;
+                    store_copy();
+                }
+            }
+        }
+        if (ok && nch > 0)
+            if ((ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_KVF), (nch - 1) & 1, abort_flag))))
+                add_sums(nch - 1);
+        float* last = STATE ? p.seg + seg_mat : (p.nseg == 1 && ps.last ? ps.last + mat : nullptr);
+        if (ok && last && a < D) {
+            float4* dst = reinterpret_cast<float4*>(last + a * D + hf * 64);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                dst[c] = make_float4(st[4 * c], st[4 * c + 1], st[4 * c + 2], st[4 * c + 3]);
+        }
     }
+#undef DBAR
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The segments' own contributions (p.seg) into the state in front of each, in
+// the order of walking, and into the state behind the last.  Thread = 4 entries.
+template <int D>
+__global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ DecayParams p) {
+    constexpr int PER = D * D / 4;
+    const int bh = blockIdx.y, pi = blockIdx.z;
+    const int e4 = blockIdx.x * 256 + threadIdx.x;  // D * D / 4 is a multiple of 256
+    const DecayPass& ps = p.pass[pi];
+    const int len = decay_len(p.lens, bh / p.H, p.N);
+    const double ld = decay_log(p.log_decay, bh % p.H);
+    const size_t mat = static_cast<size_t>(bh) * PER;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ps.init) {
+        if (ps.transposed) {
+            const int a = e4 * 4 / D, c = e4 * 4 % D;
+            const float* src = ps.init + mat * 4 + a;
+            S = make_float4(src[c * D], src[(c + 1) * D], src[(c + 2) * D], src[(c + 3) * D]);
+        } else {
+            S = reinterpret_cast<const float4*>(ps.init)[mat + e4];
+        }
+    }
+    float4* at = reinterpret_cast<float4*>(p.seg) + static_cast<size_t>(pi) * p.nseg * p.B * p.H * PER + mat + e4;
+    const size_t step = static_cast<size_t>(p.B) * p.H * PER;
+    for (int i = 0; i < p.nseg; ++i) {
+        const int seg = ps.reverse ? p.nseg - 1 - i : i;
+        int c0, c1;
+        decay_span(len, seg, p.seg_chunks, &c0, &c1);
+        const int n = min(c1 * kDecayChunk, len) - min(c0 * kDecayChunk, len);
+        const double gd = exp(ld * n);
+        const float g = static_cast<float>(gd), g2 = static_cast<float>(gd - g);
+        const float4 own = at[seg * step];
+        at[seg * step] = S;
+        S.x = fmaf(g, S.x, fmaf(g2, S.x, own.x)), S.y = fmaf(g, S.y, fmaf(g2, S.y, own.y));
+        S.z = fmaf(g, S.z, fmaf(g2, S.z, own.z)), S.w = fmaf(g, S.w, fmaf(g2, S.w, own.w));
+    }
+    if (ps.last) reinterpret_cast<float4*>(ps.last)[mat + e4] = S;
+}
+
+// Segments of a call: one, unless its CTAs (one per pass, head and 64 features)
+// fill less than half of the device's 148 multiprocessors; then as many as fit,
+// of four chunks at least (a segment costs a second pass over y and z, and a
+// state written and read).
+inline void decay_segments(int B, int H, int N, int d, int passes, int* nseg, int* seg_chunks) {
+    const long long ctas = 1LL * passes * B * H * (d / 64);
+    const int chunks = (N + kDecayChunk - 1) / kDecayChunk;
+    long long n = ctas * 2 <= 148 ? 148 / ctas : 1;
+    if (n > chunks / 4) n = chunks / 4;
+    if (n < 1) n = 1;
+    *seg_chunks = static_cast<int>((chunks + n - 1) / n);
+    *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
+}
+
+inline size_t decay_workspace(int B, int H, int N, int d, int passes) {
+    int nseg, seg_chunks;
+    decay_segments(B, H, N, d, passes, &nseg, &seg_chunks);
+    return nseg > 1 ? static_cast<size_t>(passes) * nseg * B * H * d * d * 4 : 0;
+}
+
+template <int D, bool BF16>
+bool decay_set_attributes() {
+    const int bytes = static_cast<int>(DecayCfg<D, BF16>::SMEM_BYTES);
+    return cudaFuncSetAttribute(decay_chunk_kernel<D, BF16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(decay_chunk_kernel<D, BF16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes) == cudaSuccess;
+}
+
+template <int D, bool BF16>
+void decay_launch(const DecayMaps& maps, const DecayParams& p, cudaStream_t st) {
+    constexpr uint32_t bytes = DecayCfg<D, BF16>::SMEM_BYTES;
+    const unsigned grid = static_cast<unsigned>(p.B) * p.H * (D / 64) * p.passes * p.nseg;
+    if (p.nseg > 1) {
+        decay_chunk_kernel<D, BF16, true><<<grid, 448, bytes, st>>>(maps, p);
+        decay_scan_kernel<D><<<dim3(D * D / 1024, p.B * p.H, p.passes), 256, 0, st>>>(p);
+    }
+    decay_chunk_kernel<D, BF16, false><<<grid, 448, bytes, st>>>(maps, p);
 }
 
 // One token: one CTA per head, thread = column of the state.

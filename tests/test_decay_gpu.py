@@ -4,7 +4,9 @@ reference.
 Tolerances, relative L2 per head.  A 16-bit result passes three roundings to its
 type (the in-chunk weights, the state's copy for the tensor cores, the result),
 each uniform within half a step eps/2 and so eps/2/sqrt(3) in L2; three independent
-ones make eps/2.  States are fp32; their terms reach the tensor cores in two 16-bit
+ones make eps/2.  A head of few tokens has too few roundings to average: the weight of
+a single token is one number, its rounding, up to eps/2, is the whole row's, and the
+result's own comes on top, so there each of the three counts in full, 3 eps/2.  States are fp32; their terms reach the tensor cores in two 16-bit
 pieces (2^-16 of a term at most for bf16), and fp32 sums of n terms add about
 sqrt(n) 2^-24: 2e-5.  A step rounds its result once and its state by a few 2^-24.
 """
@@ -33,12 +35,17 @@ def ints(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def close(got, want, tol, label):
+FEW = 16
+
+
+def close(got, want, tol, label, chunked=True):
     """Every head's relative L2; NaN in `want` marks rows that hold 7 still."""
+    top = tol
     for b in range(want.shape[0]):
         for h in range(want.shape[1]):
             g, w = got[b, h], want[b, h]
             gone = np.isnan(w)
+            tol = 3 * top if chunked and (~gone[:, 0]).sum() < FEW else top
             assert np.all(g[gone] == 7.0), f"{label} {(b, h)}: a row past the end was written"
             g, w = g[~gone], w[~gone]
             assert np.all(np.isfinite(g)), f"{label} {(b, h)}"
@@ -159,7 +166,7 @@ def test_step(B, H, d, dtype):
     ld = decays(H)
     want, s_want = ref.decay_forward(f64(q), f64(k), f64(v), f64(ld), f64(s0), [1] * B, 0.3)
     o, s1 = attn.decay_step(q, k, v, ld, s0, 0.3)
-    close(f64(o), want, half(dtype), "o")
+    close(f64(o), want, half(dtype), "o", chunked=False)
     close(f64(s1), s_want, 2.0 ** -22, "state")
     keep = s0.clone()
     o2, s2 = attn.decay_step(q, k, v, ld, keep, 0.3, state_out=keep)  # in place
@@ -183,7 +190,7 @@ def test_prompt_then_tokens_is_the_whole_sequence(d, dtype):
         cut = lambda x: torch.stack([x[b, :, n + i] for b, n in enumerate(lens)])[:, :, None].contiguous()  # noqa: E731
         o, _ = attn.decay_step(cut(q), cut(k), cut(v), ld, state, state_out=state)
         now = np.stack([want[b, :, n + i] for b, n in enumerate(lens)])[:, :, None]
-        close(f64(o), now, half(dtype), f"token {i}")
+        close(f64(o), now, half(dtype), f"token {i}", chunked=False)
     close(f64(state), s_want, STATE_TOL, "state")
 
 
@@ -215,7 +222,7 @@ def test_hybrid_decoder_layers_run_together():
         for dst, src in zip(now, (q, k, v)):
             dst.copy_(src[:, :, t:t + 1])
         graph.replay()
-        close(f64(b), lin[:, :, t:t + 1], half("bf16"), f"token {t}")
+        close(f64(b), lin[:, :, t:t + 1], half("bf16"), f"token {t}", chunked=False)
         c = [f64(x) for x in cache]
         want, _, w, mag = ref.attend(f64(now[0]), *c, table.cpu().numpy(), [t + 1] * B, [1] * B, True,
                                      1 / math.sqrt(d))
