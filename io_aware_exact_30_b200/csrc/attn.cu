@@ -129,6 +129,8 @@ int check_device(int* dev_out) {
     ok &= cudaFuncSetAttribute(attn::linear_fused_kernel<false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                attn::LinFusedCfg::SMEM_BYTES) == cudaSuccess;
+    ok &= attn::attend_set_attributes<64, true>() && attn::attend_set_attributes<64, false>() &&
+          attn::attend_set_attributes<128, true>() && attn::attend_set_attributes<128, false>();
     ok &= attn::decay_set_attributes<64, true>() && attn::decay_set_attributes<64, false>() &&
           attn::decay_set_attributes<128, true>() && attn::decay_set_attributes<128, false>();
     ok &= attn::bwd_set_attributes();
@@ -930,7 +932,7 @@ int check_attend(int B, int Hq, int Hkv, int T, int d, int dtype, float scale) {
 extern "C" size_t attn_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int T, int d,
                                                     int max_len) {
     if (check_attend(B, Hq, Hkv, T, d, ATTN_BF16, 1.f) || max_len < 1) return 0;
-    return 0;
+    return attn::attend_workspace(B, Hq, Hkv, T, d, max_len);
 }
 
 extern "C" int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned char* v8,
@@ -962,18 +964,22 @@ extern "C" int attn_cache_attend(const void* q, const unsigned char* k8, const u
     p.table = page_table, p.lens = lens, p.q_lens = q_lens;
     p.o = static_cast<uint8_t*>(o), p.lse = lse;
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T;
-    p.num_pages = num_pages, p.page = page, p.max_pages = max_pages;
+    p.num_pages = num_pages, p.max_pages = max_pages;
+    p.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
+    p.mtiles = attn::attend_mtiles(Hq, Hkv, T);
+    attn::attend_splits(B, Hkv, p.mtiles, max_len, &p.nsplit, &p.split);
+    if (1LL * p.mtiles * p.nsplit * Hkv * B >= (1LL << 31)) return ATTN_ERR_SHAPE;
+    if (p.nsplit > 1 && !workspace) return ATTN_ERR_NULL;
+    p.part = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part + static_cast<size_t>(B) * Hq * T * p.nsplit * d);
     p.causal = causal ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned g = static_cast<unsigned>((1LL * B * Hq * T + 3) / 4);
     const bool bf = dtype == ATTN_BF16;
     if (d == 64)
-        bf ? attn::cache_attend_rows_kernel<64, true><<<g, 128, 0, st>>>(p)
-           : attn::cache_attend_rows_kernel<64, false><<<g, 128, 0, st>>>(p);
+        bf ? attn::attend_launch<64, true>(p, st) : attn::attend_launch<64, false>(p, st);
     else
-        bf ? attn::cache_attend_rows_kernel<128, true><<<g, 128, 0, st>>>(p)
-           : attn::cache_attend_rows_kernel<128, false><<<g, 128, 0, st>>>(p);
+        bf ? attn::attend_launch<128, true>(p, st) : attn::attend_launch<128, false>(p, st);
     return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 

@@ -153,72 +153,488 @@ struct AttendParams {
     const int* q_lens;     // queries of each sequence; null: T
     uint8_t* o;
     float* lse;
-    int B, Hq, Hkv, T, num_pages, page, max_pages;
+    float* part;           // split sequences: (row, split, D) fp32, not normalised
+    float2* part_ml;       // (row, split): maximum (log2 units) and sum
+    int B, Hq, Hkv, T, num_pages, page_shift, max_pages;
+    int mtiles;            // 16-row tiles of the G T query rows of a key/value head
+    int nsplit, split;     // splits of `split` tokens; the last takes what is left
     int causal;
     float scale_log2;
 };
 
-// One warp per query row: keys one by one, the online softmax in every lane,
-// lane l holding D / 32 features.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Two e4m3 codes (low half of v, or the high one) as two fp16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t v, bool high) {
+    uint32_t r;
+    const uint16_t h = static_cast<uint16_t>(high ? v >> 16 : v);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
+    return r;
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void attend_lengths(const AttendParams& p, int b, int* len, int* tb, bool report) {
+    const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
+    int n = p.lens[b], t = p.q_lens ? p.q_lens[b] : p.T;
+    if (n < 0 || n > cap || t < 0 || t > p.T) {
+        if (report) record_bad_page();
+        n = n < 0 ? 0 : (n > cap ? static_cast<int>(cap) : n);
+        t = t < 0 ? 0 : (t > p.T ? p.T : t);
+    }
+    *len = n;
+    *tb = t;
+}
+
+// One CTA per (16 query rows, split, key/value head, sequence); the G T rows of a
+// key/value head (G query heads share it) are one matrix, so its codes are read
+// once for up to 16 of them.  Four warps take 32-key steps in turn, each with its
+// own running maximum, sum and output, joined at the end.
+//
+// Both products run on fp16 tensor-core fragments (m16n8k16): a single token is a
+// handful of rows, far too few for the 128 of a tensor-memory tile, and what
+// bounds the kernel is the codes' way from HBM.  e4m3 converts to fp16 exactly.
+// q is brought into fp16 by a power of two for each row (its largest value in
+// 8..16): exact down to 2^-18 of it.  P is at most 1 and goes to fp16 rounded
+// (half a step, 2^-11).  Page scales are applied in fp32: that of K to the scores, that of V
+// to the step's own product before it is added to the output.
+//
+// A fragment's K extent is a sum, in any order, so the lanes take features and
+// keys in the order in which 16-byte pieces lie in memory: of a K row lane t
+// (t = lane % 4) takes features 16 t .. 16 t + 15 of each 64, of V rows 2t, 2t+1,
+// 2t+8, 2t+9 lane (g, t) (g = lane / 4) takes features D/8 g .., and a byte
+// permute pairs two keys' codes.  Each lane thus reads, through shared memory, only what
+// it copied itself (cp.async): no barrier but its own copies'.
+template <int D>
+struct AttendCfg {
+    static constexpr int KP = D / 32, VP = 4;  // pieces of 16 keys: K 16 bytes each, V D/8 bytes
+    static constexpr int VW = D / 32;          // words of a V piece
+    static constexpr uint32_t V_OFF = KP * 512u, TILE = V_OFF + VP * 32u * (D / 8);
+    static constexpr int STAGES = D == 128 ? 2 : 3;  // steps of two 16-key tiles
+    static constexpr uint32_t WARP = STAGES * 2 * TILE;
+    static constexpr uint32_t SMEM = 4 * WARP;
+    static_assert(SMEM >= 4 * 16 * (D + 4) * 4 + 4 * 16 * 8, "room for the join");
+};
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) cache_attend_rows_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(128, D == 128 ? 3 : 4) cache_attend_kernel(const AttendParams p) {
+    using C = AttendCfg<D>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    int id = blockIdx.x;
+    const int mt = id % p.mtiles;
+    id /= p.mtiles;
+    const int split = id % p.nsplit;
+    id /= p.nsplit;
+    const int hk = id % p.Hkv, b = id / p.Hkv;
+    int len, tb;
+    attend_lengths(p, b, &len, &tb, threadIdx.x == 0);
+    const int G = p.Hq / p.Hkv, rows = G * tb;  // row r: query r / G of head hk G + r % G
+    const int k0 = split * p.split;
+    if (mt * 16 >= rows || (split > 0 && k0 >= len)) return;
+    const int k1 = split == p.nsplit - 1 ? len : min(len, k0 + p.split);
+    const bool whole = p.nsplit == 1 || len <= p.split;
+    // keys that this lane's two rows see, and that all 16 rows see
+    int see[2];
+    int all = len;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = mt * 16 + g + 8 * i;
+        see[i] = r < rows ? (p.causal ? len - (tb - 1 - r / G) : len) : 0;
+    }
+    if (p.causal) all = len - (tb - 1 - mt * 16 / G);
+    // ------------------------------------------------------------ queries
+    uint32_t qf[D / 16][4];
+    float mul[2];
+    {
+        uint4 raw[2][D / 32];  // features 64 h + 16 t4 .. + 15 of the two rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = mt * 16 + g + 8 * i;
+            uint32_t top = 0u;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                raw[i][c] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) {
+                    const size_t row = (static_cast<size_t>(b) * p.Hq + hk * G + r % G) * p.T + r / G;
+                    raw[i][c] = __ldg(reinterpret_cast<const uint4*>(
+                        p.q + (row * D + 64 * (c >> 1) + 16 * t4 + 8 * (c & 1)) * 2));
+                }
+                top = __vmaxu2(__vmaxu2(top, raw[i][c].x & 0x7fff7fffu), raw[i][c].y & 0x7fff7fffu);
+                top = __vmaxu2(__vmaxu2(top, raw[i][c].z & 0x7fff7fffu), raw[i][c].w & 0x7fff7fffu);
+            }
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float2 f = unpack2<BF16>(top);
+            // 2^k with the row's largest magnitude times it in 8 .. 16
+            int e = 130 - static_cast<int>(__float_as_uint(fmaxf(f.x, f.y)) >> 23);
+            e = e < -126 ? -126 : (e > 126 ? 126 : e);
+            const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+            mul[i] = p.scale_log2 * (1.f / up);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const uint32_t w[4] = {raw[i][c].x, raw[i][c].y, raw[i][c].z, raw[i][c].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = unpack2<BF16>(w[j]);
+                    // k-step 2 c + j / 2 has features 4 (2 c + j / 2) ..; pair j % 2
+                    qf[2 * c + (j >> 1)][i + 2 * (j & 1)] = pack2<false>(x.x * up, x.y * up);
+                }
+            }
+        }
+    }
+    // --------------------------------------------- this warp's 16-key tiles
+    // Step s covers tiles 2 (4 s + warp) and the next; lane l looks up the page and
+    // scales of tiles l of 32 at a time (16 steps), one batch ahead.
+    const int tile0 = k0 >> 4, ntiles = (k1 - k0 + 15) >> 4;  // splits start at tiles
+    const int nsteps = (ntiles + 7 - 2 * warp) >> 3;          // of this warp
+    auto tile_of = [&](int s, int u) { return tile0 + 8 * s + 2 * warp + u; };
+    auto look_up = [&](int batch, int& page, float& ks, float& vs) {
+        const int tile = tile_of(batch * 16 + (lane >> 1), lane & 1);
+        page = -1;
+        ks = vs = 0.f;
+        if (tile - tile0 < ntiles) {
+            page = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + (tile >> (p.page_shift - 4)));
+            if (page < 0 || page >= p.num_pages) {
+                record_bad_page();
+                page = -1;
+            } else {
+                const size_t at = static_cast<size_t>(page) * p.Hkv + hk;
+                ks = __ldg(p.scale[0] + at);
+                vs = __ldg(p.scale[1] + at);
+            }
+        }
+    };
+    int page_a, page_b;
+    float ks_a, vs_a, ks_b, vs_b;
+    look_up(0, page_a, ks_a, vs_a);
+    page_b = -1, ks_b = vs_b = 0.f;
+    if (nsteps > 16) look_up(1, page_b, ks_b, vs_b);
+    const uint32_t ring = smem_u32(smem_raw) + warp * C::WARP;
+    int batch = 0;  // the batch that page_a holds
+    auto load = [&](int s) {
+        if (s < nsteps) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int pa = __shfl_sync(0xffffffffu, page_a, (s & 15) * 2 + u);
+                const int pb = __shfl_sync(0xffffffffu, page_b, (s & 15) * 2 + u);
+                const int page = (s >> 4) == batch ? pa : pb;
+                if (page >= 0) {
+                    const int slot = (tile_of(s, u) << 4) & ((1 << p.page_shift) - 1);
+                    const size_t at =
+                        ((static_cast<size_t>(page) * p.Hkv + hk) << p.page_shift) + static_cast<size_t>(slot);
+                    const uint32_t dst = ring + ((s % C::STAGES) * 2 + u) * C::TILE;
+                    const uint8_t* k = p.codes[0] + at * D + g * D + t4 * 16;
+#pragma unroll
+                    for (int i = 0; i < C::KP; ++i)  // keys g + 8 (i % 2), features 64 (i / 2) ..
+                        cp_async16(dst + i * 512u + lane * 16u, k + (i & 1) * 8 * D + (i >> 1) * 64);
+                    const uint8_t* v = p.codes[1] + at * D + 2 * t4 * D + g * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                        const uint32_t d = dst + C::V_OFF + (i * 32u + lane) * (D / 8);
+                        const uint8_t* src = v + ((i & 1) + (i >> 1) * 8) * D;
+                        if constexpr (D == 128) cp_async16(d, src); else cp_async8(d, src);
+                    }
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < C::STAGES; ++s) load(s);
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int s = 0; s < nsteps; ++s) {
+        int page[2];
+        float ks[2], vs[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            page[u] = __shfl_sync(0xffffffffu, page_a, (s & 15) * 2 + u);
+            ks[u] = __shfl_sync(0xffffffffu, ks_a, (s & 15) * 2 + u);
+            vs[u] = __shfl_sync(0xffffffffu, vs_a, (s & 15) * 2 + u);
+        }
+        cp_async_wait<C::STAGES - 1>();
+        const uint8_t* buf = smem_raw + warp * C::WARP + (s % C::STAGES) * 2 * C::TILE;
+        const int key0 = tile_of(s, 0) << 4;
+        // ------------------------------------------------------- scores
+        float x[2][2][4];  // tile, 8 keys, (row, key pair)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[u][nb][e] = 0.f;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    const uint4 w4 = *reinterpret_cast<const uint4*>(buf + u * C::TILE + (h * 2 + nb) * 512 + lane * 16);
+                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_f16(x[u][nb], qf[h * 4 + j], e4m3x2(w[j], false), e4m3x2(w[j], true));
+                }
+            }
+            const float a0 = mul[0] * ks[u], a1 = mul[1] * ks[u];
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+                x[u][nb][0] *= a0, x[u][nb][1] *= a0;
+                x[u][nb][2] *= a1, x[u][nb][3] *= a1;
+            }
+        }
+        const bool edge = key0 + 32 > all || key0 + 32 > k1 || page[0] < 0 || page[1] < 0;
+        if (edge) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + 16 * u + 8 * nb + 2 * t4 + (e & 1);
+                        if (page[u] < 0 || key >= see[e >> 1] || key >= k1) x[u][nb][e] = -INFINITY;
+                    }
+        }
+        // ------------------------------------------------------- softmax
+        float top[2], base[2], keep[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v = m[i];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                v = fmaxf(fmaxf(fmaxf(v, x[u][0][2 * i]), fmaxf(x[u][0][2 * i + 1], x[u][1][2 * i])),
+                          x[u][1][2 * i + 1]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            top[i] = v;
+            base[i] = v == -INFINITY ? 0.f : v;  // a row that sees nothing yet
+            keep[i] = ex2(m[i] - base[i]);
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][0] *= keep[0], o[j][1] *= keep[0];
+                o[j][2] *= keep[1], o[j][3] *= keep[1];
+            }
+            l[0] *= keep[0], l[1] *= keep[1];
+            m[0] = top[0], m[1] = top[1];
+        }
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float p0 = ex2(x[u][nb][2 * i] - base[i]), p1 = ex2(x[u][nb][2 * i + 1] - base[i]);
+                    l[i] += p0 + p1;
+                    pf[u][2 * nb + i] = pack2<false>(p0, p1);
+                }
+        // -------------------------------------------------------- P V
+        uint32_t vw[2][4][C::VW];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* src = buf + u * C::TILE + C::V_OFF + (i * 32 + lane) * (D / 8);
+                if constexpr (D == 128) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(src);
+                    vw[u][i][0] = w.x, vw[u][i][1] = w.y, vw[u][i][2] = w.z, vw[u][i][3] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(src);
+                    vw[u][i][0] = w.x, vw[u][i][1] = w.y;
+                }
+                // slots that hold no token of this sequence may hold anything, NaN included
+                if (edge && (page[u] < 0 || key0 + 16 * u + 2 * t4 + (i & 1) + (i >> 1) * 8 >= len)) {
+#pragma unroll
+                    for (int w = 0; w < C::VW; ++w) vw[u][i][w] = 0u;
+                }
+            }
+#pragma unroll
+        for (int w = 0; w < C::VW; ++w) {
+            float sum[4][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (u == 0 || vs[0] != vs[1]) {
+                    if (u == 1) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[4 * w + j][e] = fmaf(vs[0], sum[j][e], o[4 * w + j][e]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[j][e] = 0.f;
+                }
+                const uint32_t lo0 = __byte_perm(vw[u][0][w], vw[u][1][w], 0x5140),
+                               hi0 = __byte_perm(vw[u][0][w], vw[u][1][w], 0x7362),
+                               lo1 = __byte_perm(vw[u][2][w], vw[u][3][w], 0x5140),
+                               hi1 = __byte_perm(vw[u][2][w], vw[u][3][w], 0x7362);
+                mma_f16(sum[0], pf[u], e4m3x2(lo0, false), e4m3x2(lo1, false));
+                mma_f16(sum[1], pf[u], e4m3x2(lo0, true), e4m3x2(lo1, true));
+                mma_f16(sum[2], pf[u], e4m3x2(hi0, false), e4m3x2(hi1, false));
+                mma_f16(sum[3], pf[u], e4m3x2(hi0, true), e4m3x2(hi1, true));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[4 * w + j][e] = fmaf(vs[1], sum[j][e], o[4 * w + j][e]);
+        }
+        load(s + C::STAGES);
+        if ((s & 15) == 15) {  // the next 16 steps
+            ++batch;
+            page_a = page_b, ks_a = ks_b, vs_a = vs_b;
+            page_b = -1;
+            if ((batch + 1) * 16 < nsteps) look_up(batch + 1, page_b, ks_b, vs_b);
+        }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    // ------------------------------------------------- the four warps' join
+    __syncthreads();  // every warp is done with its ring
+    constexpr int LD = D + 4;
+    float* so = reinterpret_cast<float*>(smem_raw);                        // (warp, row, feature)
+    float2* sml = reinterpret_cast<float2*>(smem_raw + 4 * 16 * LD * 4);   // (warp, row)
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            so[(warp * 16 + g + 8 * (e >> 1)) * LD + (2 * t4 + (e & 1)) * (D / 8) + j] = o[j][e];
+    if (t4 == 0) {
+        sml[warp * 16 + g] = make_float2(m[0], l[0]);
+        sml[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+    }
+    __syncthreads();
+    const int r = threadIdx.x >> 3, c0 = threadIdx.x & 7;  // eight threads a row
+    if (mt * 16 + r >= rows) return;
+    float mm = -INFINITY, ll = 0.f, f[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sml[w * 16 + r].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float2 ml = sml[w * 16 + r];
+        f[w] = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
+        ll += f[w] * ml.y;
+    }
+    const int rr = mt * 16 + r;
+    const size_t row = (static_cast<size_t>(b) * p.Hq + hk * G + rr % G) * p.T + rr / G;
+    const float inv = whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        const int c = (c0 + 8 * k) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float4 a = *reinterpret_cast<const float4*>(so + (w * 16 + r) * LD + c);
+            v.x = fmaf(f[w], a.x, v.x), v.y = fmaf(f[w], a.y, v.y);
+            v.z = fmaf(f[w], a.z, v.z), v.w = fmaf(f[w], a.w, v.w);
+        }
+        if (whole)
+            *reinterpret_cast<uint2*>(p.o + (row * D + c) * 2) =
+                make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+        else
+            *reinterpret_cast<float4*>(p.part + (row * p.nsplit + split) * D + c) = v;
+    }
+    if (c0 == 0) {
+        if (whole)
+            p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        else
+            p.part_ml[row * p.nsplit + split] = make_float2(mm, ll);
+    }
+}
+
+// Joins the splits of a row: one warp a row, lane l holding D / 32 features.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) cache_attend_join_kernel(const AttendParams p) {
     constexpr int E = D / 32;
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= static_cast<long long>(p.B) * p.Hq * p.T) return;
-    const int t = static_cast<int>(row % p.T);
-    const int hq = static_cast<int>(row / p.T % p.Hq), b = static_cast<int>(row / p.T / p.Hq);
-    const int hk = hq / (p.Hq / p.Hkv);
-    const long long cap = static_cast<long long>(p.max_pages) * p.page;
-    int len = p.lens[b], tb = p.q_lens ? p.q_lens[b] : p.T;
-    if (len < 0 || len > cap || tb < 0 || tb > p.T) {
-        if (lane == 0) record_bad_page();
-        len = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
-        tb = tb < 0 ? 0 : (tb > p.T ? p.T : tb);
+    const int t = static_cast<int>(row % p.T), b = static_cast<int>(row / p.T / p.Hq);
+    int len, tb;
+    attend_lengths(p, b, &len, &tb, false);
+    if (t >= tb || len <= p.split) return;  // no such query, or one split: stored already
+    const int n = min(p.nsplit, (len + p.split - 1) / p.split);
+    const float2* ml = p.part_ml + row * p.nsplit;
+    float mm = -INFINITY;
+    for (int i = lane; i < n; i += 32) mm = fmaxf(mm, ml[i].x);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
+    float acc[E], ll = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float2 v = ml[i];
+        const float w = v.x == -INFINITY ? 0.f : ex2(v.x - mm);
+        ll = fmaf(w, v.y, ll);
+        const float* src = p.part + (row * p.nsplit + i) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, src[e], acc[e]);
     }
-    if (t >= tb) return;
-    const int end = p.causal ? len - (tb - 1 - t) : len;
-    float qv[E], acc[E];
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        const float2 f = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(p.q + (row * D + lane * E + e) * 2));
-        qv[e] = f.x, qv[e + 1] = f.y;
-        acc[e] = acc[e + 1] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < end; ++j) {
-        const int id_page = p.table[static_cast<size_t>(b) * p.max_pages + j / p.page];
-        if (id_page < 0 || id_page >= p.num_pages) {
-            if (lane == 0) record_bad_page();
-            continue;
-        }
-        const size_t slot = static_cast<size_t>(id_page) * p.Hkv + hk;
-        const size_t at = (slot * p.page + j % p.page) * D + lane * E;
-        float kx[E], vx[E], dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            __nv_fp8_e4m3 c;
-            c.__x = p.codes[0][at + e];
-            kx[e] = static_cast<float>(c);
-            c.__x = p.codes[1][at + e];
-            vx[e] = static_cast<float>(c) * p.scale[1][slot];
-            dot += qv[e] * kx[e];
-        }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-        const float x = dot * p.scale[0][slot] * p.scale_log2;
-        const float m2 = fmaxf(m, x), a = exp2f(m - m2), w = exp2f(x - m2);
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * vx[e];
-        m = m2;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(p.o + (row * D + lane * E + e) * 2) =
-            pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        *reinterpret_cast<uint32_t*>(p.o + (row * D + lane * E + e) * 2) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Splits of a call whose sequences hold at most max_len tokens: enough CTAs to
+// fill the device's 148 multiprocessors several times over (uneven lengths even
+// out), but no split below 256 tokens, where joining costs more than it gives.
+inline void attend_splits(int B, int Hkv, int mtiles, int max_len, int* nsplit, int* split) {
+    if (max_len > (1 << 30)) max_len = 1 << 30;  // split * nsplit stays an int
+    const long long base = 1LL * B * Hkv * mtiles;
+    const long long want = (148 * 3 * 4 + base - 1) / base;  // splits for about four rounds of CTAs
+    long long len = (max_len + want - 1) / want;
+    len = (len + 127) / 128 * 128;
+    if (len < 256) len = 256;
+    *nsplit = static_cast<int>((max_len + len - 1) / len);
+    *split = static_cast<int>(len);
+}
+
+inline int attend_mtiles(int Hq, int Hkv, int T) { return (Hq / Hkv * T + 15) / 16; }
+
+inline size_t attend_workspace(int B, int Hq, int Hkv, int T, int D, int max_len) {
+    int nsplit, split;
+    attend_splits(B, Hkv, attend_mtiles(Hq, Hkv, T), max_len, &nsplit, &split);
+    return nsplit > 1 ? static_cast<size_t>(B) * Hq * T * nsplit * (D + 2) * 4 : 0;
+}
+
+template <int D, bool BF16>
+bool attend_set_attributes() {
+    return cudaFuncSetAttribute(cache_attend_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(AttendCfg<D>::SMEM)) == cudaSuccess;
+}
+
+template <int D, bool BF16>
+void attend_launch(const AttendParams& p, cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>(p.mtiles) * p.nsplit * p.Hkv * p.B;
+    cache_attend_kernel<D, BF16><<<grid, 128, AttendCfg<D>::SMEM, st>>>(p);
+    if (p.nsplit > 1) {
+        const long long rows = 1LL * p.B * p.Hq * p.T;
+        cache_attend_join_kernel<D, BF16><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
+    }
 }
 
 }  // namespace attn
