@@ -156,7 +156,7 @@ struct AttendParams {
     float* part;           // split sequences: (row, split, D) fp32, not normalised
     float2* part_ml;       // (row, split): maximum (log2 units) and sum
     int B, Hq, Hkv, T, num_pages, page_shift, max_pages;
-    int mtiles;            // 16-row tiles of the G T query rows of a key/value head
+    int mtiles;            // CTAs for the G T query rows of a key/value head
     int nsplit, split;     // splits of `split` tokens; the last takes what is left
     int causal;
     float scale_log2;
@@ -180,12 +180,24 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t v, bool high) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
     return r;
 }
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16.
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16; and the same from zero.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_from0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Transposes an 8 x 8 matrix of 16-bit values held as a fragment.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 __device__ __forceinline__ void attend_lengths(const AttendParams& p, int b, int* len, int* tb, bool report) {
@@ -200,39 +212,49 @@ __device__ __forceinline__ void attend_lengths(const AttendParams& p, int b, int
     *tb = t;
 }
 
-// One CTA per (16 query rows, split, key/value head, sequence); the G T rows of a
-// key/value head (G query heads share it) are one matrix, so its codes are read
-// once for up to 16 of them.  Four warps take 32-key steps in turn, each with its
+// One CTA per (8 NT query rows, split, key/value head, sequence); the G T rows of
+// a key/value head (G query heads share it) are one matrix, so its codes are read
+// once for up to 16 of them.  Four warps take 16-key tiles in turn, each with its
 // own running maximum, sum and output, joined at the end.
 //
-// Both products run on fp16 tensor-core fragments (m16n8k16): a single token is a
-// handful of rows, far too few for the 128 of a tensor-memory tile, and what
-// bounds the kernel is the codes' way from HBM.  e4m3 converts to fp16 exactly.
-// q is brought into fp16 by a power of two for each row (its largest value in
-// 8..16): exact down to 2^-18 of it.  P is at most 1 and goes to fp16 rounded
-// (half a step, 2^-11).  Page scales are applied in fp32: that of K to the scores, that of V
-// to the step's own product before it is added to the output.
+// Both products run on fp16 tensor-core fragments (m16n8k16), transposed: S^T =
+// K Q^T and O^T = V^T P^T, the query rows in the narrow (8) extent.  A single
+// token is a handful of rows, far too few for the 128 of a tensor-memory tile,
+// and what bounds the kernel is the codes' way from HBM and through the registers.
+//   e4m3 converts to fp16 exactly.  q is brought into fp16 by a power of two for
+// each row (its largest value in 8..16): exact down to 2^-18 of it.  P goes to
+// fp16 rounded (half a step, 2^-11).  The running maximum of a row stays until a
+// score exceeds it by more than 2^6 (all exponents and the final division use the
+// same one), so P is at most 2^6; it is stored times 2^9, which leaves everything
+// above 2^-23 of the maximum's weight in fp16's normal range.
+//   The scale of K's page multiplies the scores in fp32.  O is kept in units of the
+// largest scale u of V met so far: the scale s of a tile's page enters P as the
+// factor s / u, or, below 2^-6, where P would leave fp16's range, the
+// tile's own product in fp32.
 //
 // A fragment's K extent is a sum, in any order, so the lanes take features and
-// keys in the order in which 16-byte pieces lie in memory: of a K row lane t
-// (t = lane % 4) takes features 16 t .. 16 t + 15 of each 64, of V rows 2t, 2t+1,
-// 2t+8, 2t+9 lane (g, t) (g = lane / 4) takes features D/8 g .., and a byte
-// permute pairs two keys' codes.  Each lane thus reads, through shared memory, only what
+// keys in the order in which 16-byte pieces lie in memory: lane (g, t) (g = lane /
+// 4, t = lane % 4) takes of K row g (and g + 8) features 16 t .. 16 t + 15 of each
+// 64, and of V rows 2t, 2t+1, 2t+8, 2t+9 the features D/8 g .., a byte permute
+// pairing two keys' codes.  Each lane thus reads, through shared memory, only what
 // it copied itself (cp.async): no barrier but its own copies'.
-template <int D>
+template <int D, int NT>
 struct AttendCfg {
     static constexpr int KP = D / 32, VP = 4;  // pieces of 16 keys: K 16 bytes each, V D/8 bytes
     static constexpr int VW = D / 32;          // words of a V piece
     static constexpr uint32_t V_OFF = KP * 512u, TILE = V_OFF + VP * 32u * (D / 8);
-    static constexpr int STAGES = D == 128 ? 2 : 3;  // steps of two 16-key tiles
-    static constexpr uint32_t WARP = STAGES * 2 * TILE;
-    static constexpr uint32_t SMEM = 4 * WARP;
-    static_assert(SMEM >= 4 * 16 * (D + 4) * 4 + 4 * 16 * 8, "room for the join");
+    static constexpr int STAGES = D == 128 ? (NT == 1 ? 3 : 4) : 6;
+    static constexpr uint32_t WARP = STAGES * TILE;
+    static constexpr int ROWS = 8 * NT, LD = D + 4;
+    static constexpr uint32_t JOIN = 4 * ROWS * LD * 4 + 4 * ROWS * 8;
+    static constexpr uint32_t SMEM = 4 * WARP > JOIN ? 4 * WARP : JOIN;
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128, D == 128 ? 3 : 4) cache_attend_kernel(const AttendParams p) {
-    using C = AttendCfg<D>;
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) cache_attend_kernel(const AttendParams p) {
+    using C = AttendCfg<D, NT>;
+    constexpr int ROWS = C::ROWS;
+    constexpr float kRaise = 6.f, kUp = 9.f;  // log2 of P's bound and of its storage factor
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     int id = blockIdx.x;
@@ -245,69 +267,19 @@ __global__ void __launch_bounds__(128, D == 128 ? 3 : 4) cache_attend_kernel(con
     attend_lengths(p, b, &len, &tb, threadIdx.x == 0);
     const int G = p.Hq / p.Hkv, rows = G * tb;  // row r: query r / G of head hk G + r % G
     const int k0 = split * p.split;
-    if (mt * 16 >= rows || (split > 0 && k0 >= len)) return;
+    if (mt * ROWS >= rows || (split > 0 && k0 >= len)) return;
     const int k1 = split == p.nsplit - 1 ? len : min(len, k0 + p.split);
     const bool whole = p.nsplit == 1 || len <= p.split;
-    // keys that this lane's two rows see, and that all 16 rows see
-    int see[2];
-    int all = len;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = mt * 16 + g + 8 * i;
-        see[i] = r < rows ? (p.causal ? len - (tb - 1 - r / G) : len) : 0;
-    }
-    if (p.causal) all = len - (tb - 1 - mt * 16 / G);
-    // ------------------------------------------------------------ queries
-    uint32_t qf[D / 16][4];
-    float mul[2];
-    {
-        uint4 raw[2][D / 32];  // features 64 h + 16 t4 .. + 15 of the two rows
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = mt * 16 + g + 8 * i;
-            uint32_t top = 0u;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                raw[i][c] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows) {
-                    const size_t row = (static_cast<size_t>(b) * p.Hq + hk * G + r % G) * p.T + r / G;
-                    raw[i][c] = __ldg(reinterpret_cast<const uint4*>(
-                        p.q + (row * D + 64 * (c >> 1) + 16 * t4 + 8 * (c & 1)) * 2));
-                }
-                top = __vmaxu2(__vmaxu2(top, raw[i][c].x & 0x7fff7fffu), raw[i][c].y & 0x7fff7fffu);
-                top = __vmaxu2(__vmaxu2(top, raw[i][c].z & 0x7fff7fffu), raw[i][c].w & 0x7fff7fffu);
-            }
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float2 f = unpack2<BF16>(top);
-            // 2^k with the row's largest magnitude times it in 8 .. 16
-            int e = 130 - static_cast<int>(__float_as_uint(fmaxf(f.x, f.y)) >> 23);
-            e = e < -126 ? -126 : (e > 126 ? 126 : e);
-            const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-            mul[i] = p.scale_log2 * (1.f / up);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const uint32_t w[4] = {raw[i][c].x, raw[i][c].y, raw[i][c].z, raw[i][c].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 x = unpack2<BF16>(w[j]);
-                    // k-step 2 c + j / 2 has features 4 (2 c + j / 2) ..; pair j % 2
-                    qf[2 * c + (j >> 1)][i + 2 * (j & 1)] = pack2<false>(x.x * up, x.y * up);
-                }
-            }
-        }
-    }
     // --------------------------------------------- this warp's 16-key tiles
-    // Step s covers tiles 2 (4 s + warp) and the next; lane l looks up the page and
-    // scales of tiles l of 32 at a time (16 steps), one batch ahead.
+    // Step s is tile 4 s + warp; lane l looks up the page and scales of step l of 32
+    // at a time, one batch ahead.
     const int tile0 = k0 >> 4, ntiles = (k1 - k0 + 15) >> 4;  // splits start at tiles
-    const int nsteps = (ntiles + 7 - 2 * warp) >> 3;          // of this warp
-    auto tile_of = [&](int s, int u) { return tile0 + 8 * s + 2 * warp + u; };
+    const int nsteps = (ntiles + 3 - warp) >> 2;              // of this warp
     auto look_up = [&](int batch, int& page, float& ks, float& vs) {
-        const int tile = tile_of(batch * 16 + (lane >> 1), lane & 1);
+        const int step = batch * 32 + lane, tile = tile0 + 4 * step + warp;
         page = -1;
         ks = vs = 0.f;
-        if (tile - tile0 < ntiles) {
+        if (step < nsteps) {
             page = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + (tile >> (p.page_shift - 4)));
             if (page < 0 || page >= p.num_pages) {
                 record_bad_page();
@@ -319,233 +291,305 @@ __global__ void __launch_bounds__(128, D == 128 ? 3 : 4) cache_attend_kernel(con
             }
         }
     };
-    int page_a, page_b;
-    float ks_a, vs_a, ks_b, vs_b;
+    int page_a, page_b = -1;
+    float ks_a, vs_a, ks_b = 0.f, vs_b = 0.f;
     look_up(0, page_a, ks_a, vs_a);
-    page_b = -1, ks_b = vs_b = 0.f;
-    if (nsteps > 16) look_up(1, page_b, ks_b, vs_b);
-    const uint32_t ring = smem_u32(smem_raw) + warp * C::WARP;
-    int batch = 0;  // the batch that page_a holds
+    if (nsteps > 32) look_up(1, page_b, ks_b, vs_b);
+    uint8_t* const ring = smem_raw + warp * C::WARP;
+    const uint8_t* const kbase = p.codes[0] + g * D + t4 * 16;
+    const uint8_t* const vbase = p.codes[1] + 2 * t4 * D + g * (D / 8);
+    const uint32_t kdst = smem_u32(ring) + lane * 16u, vdst = smem_u32(ring) + C::V_OFF + lane * (D / 8);
+    int batch = 0;       // the batch that page_a holds
+    int load_slot = 0;   // ring slot of the next load
     auto load = [&](int s) {
         if (s < nsteps) {
+            const int page = __shfl_sync(0xffffffffu, (s >> 5) == batch ? page_a : page_b, s & 31);
+            if (page >= 0) {
+                const int slot = ((tile0 + 4 * s + warp) << 4) & ((1 << p.page_shift) - 1);
+                const size_t at =
+                    (((static_cast<size_t>(page) * p.Hkv + hk) << p.page_shift) + static_cast<size_t>(slot)) * D;
+                const uint8_t* k = kbase + at;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int pa = __shfl_sync(0xffffffffu, page_a, (s & 15) * 2 + u);
-                const int pb = __shfl_sync(0xffffffffu, page_b, (s & 15) * 2 + u);
-                const int page = (s >> 4) == batch ? pa : pb;
-                if (page >= 0) {
-                    const int slot = (tile_of(s, u) << 4) & ((1 << p.page_shift) - 1);
-                    const size_t at =
-                        ((static_cast<size_t>(page) * p.Hkv + hk) << p.page_shift) + static_cast<size_t>(slot);
-                    const uint32_t dst = ring + ((s % C::STAGES) * 2 + u) * C::TILE;
-                    const uint8_t* k = p.codes[0] + at * D + g * D + t4 * 16;
+                for (int i = 0; i < C::KP; ++i)  // keys g + 8 (i % 2), features 64 (i / 2) ..
+                    cp_async16(kdst + load_slot * C::TILE + i * 512u, k + (i & 1) * 8 * D + (i >> 1) * 64);
+                const uint8_t* v = vbase + at;
 #pragma unroll
-                    for (int i = 0; i < C::KP; ++i)  // keys g + 8 (i % 2), features 64 (i / 2) ..
-                        cp_async16(dst + i * 512u + lane * 16u, k + (i & 1) * 8 * D + (i >> 1) * 64);
-                    const uint8_t* v = p.codes[1] + at * D + 2 * t4 * D + g * (D / 8);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-                        const uint32_t d = dst + C::V_OFF + (i * 32u + lane) * (D / 8);
-                        const uint8_t* src = v + ((i & 1) + (i >> 1) * 8) * D;
-                        if constexpr (D == 128) cp_async16(d, src); else cp_async8(d, src);
-                    }
+                for (int i = 0; i < 4; ++i) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                    const uint32_t d = vdst + load_slot * C::TILE + i * 4 * D;
+                    const uint8_t* src = v + ((i & 1) + (i >> 1) * 8) * D;
+                    if constexpr (D == 128) cp_async16(d, src); else cp_async8(d, src);
                 }
             }
         }
         cp_async_commit();
+        load_slot = load_slot == C::STAGES - 1 ? 0 : load_slot + 1;
     };
 #pragma unroll
-    for (int s = 0; s < C::STAGES; ++s) load(s);
-    float o[D / 8][4];
+    for (int s = 0; s < C::STAGES - 1; ++s) load(s);
+    // ------------------------------------------------------------ queries
+    // B fragment of Q^T: row g of each 8, features as K's
+    uint32_t qf[NT][D / 16][2];
+    float up[NT];  // 2^k that brings the lane's row g into fp16
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int n = 0; n < NT; ++n) {
+        uint4 raw[D / 32];  // features 64 h + 16 t4 .. + 15
+        const int r = mt * ROWS + n * 8 + g;
+        uint32_t top = 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    for (int s = 0; s < nsteps; ++s) {
-        int page[2];
-        float ks[2], vs[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            page[u] = __shfl_sync(0xffffffffu, page_a, (s & 15) * 2 + u);
-            ks[u] = __shfl_sync(0xffffffffu, ks_a, (s & 15) * 2 + u);
-            vs[u] = __shfl_sync(0xffffffffu, vs_a, (s & 15) * 2 + u);
-        }
-        cp_async_wait<C::STAGES - 1>();
-        const uint8_t* buf = smem_raw + warp * C::WARP + (s % C::STAGES) * 2 * C::TILE;
-        const int key0 = tile_of(s, 0) << 4;
-        // ------------------------------------------------------- scores
-        float x[2][2][4];  // tile, 8 keys, (row, key pair)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[u][nb][e] = 0.f;
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    const uint4 w4 = *reinterpret_cast<const uint4*>(buf + u * C::TILE + (h * 2 + nb) * 512 + lane * 16);
-                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16(x[u][nb], qf[h * 4 + j], e4m3x2(w[j], false), e4m3x2(w[j], true));
-                }
+        for (int c = 0; c < D / 32; ++c) {
+            raw[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+                const size_t row = (static_cast<size_t>(b) * p.Hq + hk * G + r % G) * p.T + r / G;
+                raw[c] = __ldg(reinterpret_cast<const uint4*>(
+                    p.q + (row * D + 64 * (c >> 1) + 16 * t4 + 8 * (c & 1)) * 2));
             }
-            const float a0 = mul[0] * ks[u], a1 = mul[1] * ks[u];
+            top = __vmaxu2(__vmaxu2(top, raw[c].x & 0x7fff7fffu), raw[c].y & 0x7fff7fffu);
+            top = __vmaxu2(__vmaxu2(top, raw[c].z & 0x7fff7fffu), raw[c].w & 0x7fff7fffu);
+        }
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float2 f = unpack2<BF16>(top);
+        int e = 130 - static_cast<int>(__float_as_uint(fmaxf(f.x, f.y)) >> 23);
+        e = e < -126 ? -126 : (e > 126 ? 126 : e);
+        up[n] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-                x[u][nb][0] *= a0, x[u][nb][1] *= a0;
-                x[u][nb][2] *= a1, x[u][nb][3] *= a1;
+        for (int c = 0; c < D / 32; ++c) {
+            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = unpack2<BF16>(w[j]);
+                qf[n][2 * c + (j >> 1)][j & 1] = pack2<false>(x.x * up[n], x.y * up[n]);
             }
         }
-        const bool edge = key0 + 32 > all || key0 + 32 > k1 || page[0] < 0 || page[1] < 0;
-        if (edge) {
+    }
+    // of this lane's result columns, rows 2 t and 2 t + 1 of each 8: the score
+    // factor, the keys seen; and the keys that all rows see
+    float mul[NT][2];
+    int see[NT][2], all = len;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + 16 * u + 8 * nb + 2 * t4 + (e & 1);
-                        if (page[u] < 0 || key >= see[e >> 1] || key >= k1) x[u][nb][e] = -INFINITY;
-                    }
-        }
-        // ------------------------------------------------------- softmax
-        float top[2], base[2], keep[2];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float v = m[i];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                v = fmaxf(fmaxf(fmaxf(v, x[u][0][2 * i]), fmaxf(x[u][0][2 * i + 1], x[u][1][2 * i])),
-                          x[u][1][2 * i + 1]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            top[i] = v;
-            base[i] = v == -INFINITY ? 0.f : v;  // a row that sees nothing yet
-            keep[i] = ex2(m[i] - base[i]);
+            const int r = mt * ROWS + n * 8 + 2 * t4 + i;
+            mul[n][i] = p.scale_log2 / __shfl_sync(0xffffffffu, up[n], (2 * t4 + i) * 4);
+            see[n][i] = r < rows ? (p.causal ? len - (tb - 1 - r / G) : len) : 0;
         }
-        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+    if (p.causal) all = len - (tb - 1 - mt * ROWS / G);
+    if (all > k1) all = k1;
+    float o[NT][D / 16][4];
+    float m[NT][2], mb[NT][2], l[NT][2];  // maximum, the same as a base (0 for none), sum
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                o[j][0] *= keep[0], o[j][1] *= keep[0];
-                o[j][2] *= keep[1], o[j][3] *= keep[1];
-            }
-            l[0] *= keep[0], l[1] *= keep[1];
-            m[0] = top[0], m[1] = top[1];
-        }
-        uint32_t pf[2][4];
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
+            for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float p0 = ex2(x[u][nb][2 * i] - base[i]), p1 = ex2(x[u][nb][2 * i + 1] - base[i]);
-                    l[i] += p0 + p1;
-                    pf[u][2 * nb + i] = pack2<false>(p0, p1);
+        for (int i = 0; i < 2; ++i) m[n][i] = -INFINITY, mb[n][i] = l[n][i] = 0.f;
+    }
+    float unit = 0.f;
+    int slot = 0;
+    for (int s = 0; s < nsteps; ++s) {
+        const int page = __shfl_sync(0xffffffffu, page_a, s & 31);
+        const float ks = __shfl_sync(0xffffffffu, ks_a, s & 31);
+        const float vs = __shfl_sync(0xffffffffu, vs_a, s & 31);
+        load(s + C::STAGES - 1);  // into the slot that the last step has read
+        cp_async_wait<C::STAGES - 1>();
+        const uint8_t* buf = ring + slot * C::TILE;
+        slot = slot == C::STAGES - 1 ? 0 : slot + 1;
+        const int key0 = (tile0 + 4 * s + warp) << 4;
+        if (page >= 0) {
+            // --------------------------------------------------- scores
+            float x[NT][4];  // (key g, row 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                const uint4 wa = *reinterpret_cast<const uint4*>(buf + (h * 2) * 512 + lane * 16);
+                const uint4 wb = *reinterpret_cast<const uint4*>(buf + (h * 2 + 1) * 512 + lane * 16);
+                const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, c[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t f[4] = {e4m3x2(a[j], false), e4m3x2(c[j], false), e4m3x2(a[j], true),
+                                           e4m3x2(c[j], true)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (h == 0 && j == 0)
+                            mma_f16_from0(x[n], f, qf[n][0][0], qf[n][0][1]);
+                        else
+                            mma_f16(x[n], f, qf[n][h * 4 + j][0], qf[n][h * 4 + j][1]);
+                    }
                 }
-        // -------------------------------------------------------- P V
-        uint32_t vw[2][4][C::VW];
+            }
+            bool raise = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] *= mul[n][e & 1] * ks;
+            if (key0 + 16 > all) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + g + 8 * (e >> 1);
+                        if (key >= see[n][e & 1] || key >= k1) x[n][e] = -INFINITY;
+                    }
+            }
+            // -------------------------------------------------- softmax
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) raise |= fmaxf(x[n][i], x[n][i + 2]) > m[n][i] + kRaise;
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float v = fmaxf(fmaxf(x[n][i], x[n][i + 2]), m[n][i]);
+#pragma unroll
+                        for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+                        const float base = v == -INFINITY ? 0.f : v, keep = ex2(m[n][i] - base);
+                        m[n][i] = v;
+                        mb[n][i] = base;
+                        l[n][i] *= keep;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) o[n][j][i] *= keep, o[n][j][i + 2] *= keep;
+                    }
+            }
+            if (vs > unit) {
+                const float down = unit / vs;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][j][e] *= down;
+                unit = vs;
+            }
+            const float ratio = unit > 0.f ? vs / unit : 0.f;
+            const bool near = ratio >= 0.015625f;
+            // P 2^9 s / u; the sums without s / u
+            const float add = kUp + (near ? __log2f(ratio) : 0.f);
+            const float back = near ? 1.f / ratio : 1.f;
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float b0 = add - mb[n][0], b1 = add - mb[n][1];
+                const float p0 = ex2(x[n][0] + b0), p1 = ex2(x[n][1] + b1), p2 = ex2(x[n][2] + b0),
+                            p3 = ex2(x[n][3] + b1);
+                l[n][0] = fmaf(p0 + p2, back, l[n][0]);
+                l[n][1] = fmaf(p1 + p3, back, l[n][1]);
+                pf[n][0] = transpose8x8(pack2<false>(p0, p1));
+                pf[n][1] = transpose8x8(pack2<false>(p2, p3));
+            }
+            // ---------------------------------------------------- V^T P^T
+            uint32_t vw[4][C::VW];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint8_t* src = buf + u * C::TILE + C::V_OFF + (i * 32 + lane) * (D / 8);
+                const uint8_t* src = buf + C::V_OFF + (i * 32 + lane) * (D / 8);
                 if constexpr (D == 128) {
                     const uint4 w = *reinterpret_cast<const uint4*>(src);
-                    vw[u][i][0] = w.x, vw[u][i][1] = w.y, vw[u][i][2] = w.z, vw[u][i][3] = w.w;
+                    vw[i][0] = w.x, vw[i][1] = w.y, vw[i][2] = w.z, vw[i][3] = w.w;
                 } else {
                     const uint2 w = *reinterpret_cast<const uint2*>(src);
-                    vw[u][i][0] = w.x, vw[u][i][1] = w.y;
-                }
-                // slots that hold no token of this sequence may hold anything, NaN included
-                if (edge && (page[u] < 0 || key0 + 16 * u + 2 * t4 + (i & 1) + (i >> 1) * 8 >= len)) {
-#pragma unroll
-                    for (int w = 0; w < C::VW; ++w) vw[u][i][w] = 0u;
+                    vw[i][0] = w.x, vw[i][1] = w.y;
                 }
             }
+            if (key0 + 16 > len) {  // slots past the last token may hold anything, NaN included
 #pragma unroll
-        for (int w = 0; w < C::VW; ++w) {
-            float sum[4][4];
+                for (int i = 0; i < 4; ++i)
+                    if (key0 + 2 * t4 + (i & 1) + (i >> 1) * 8 >= len) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u == 0 || vs[0] != vs[1]) {
-                    if (u == 1) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[4 * w + j][e] = fmaf(vs[0], sum[j][e], o[4 * w + j][e]);
+                        for (int w = 0; w < C::VW; ++w) vw[i][w] = 0u;
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[j][e] = 0.f;
-                }
-                const uint32_t lo0 = __byte_perm(vw[u][0][w], vw[u][1][w], 0x5140),
-                               hi0 = __byte_perm(vw[u][0][w], vw[u][1][w], 0x7362),
-                               lo1 = __byte_perm(vw[u][2][w], vw[u][3][w], 0x5140),
-                               hi1 = __byte_perm(vw[u][2][w], vw[u][3][w], 0x7362);
-                mma_f16(sum[0], pf[u], e4m3x2(lo0, false), e4m3x2(lo1, false));
-                mma_f16(sum[1], pf[u], e4m3x2(lo0, true), e4m3x2(lo1, true));
-                mma_f16(sum[2], pf[u], e4m3x2(hi0, false), e4m3x2(hi1, false));
-                mma_f16(sum[3], pf[u], e4m3x2(hi0, true), e4m3x2(hi1, true));
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int w = 0; w < C::VW; ++w) {
+                const uint32_t lo0 = __byte_perm(vw[0][w], vw[1][w], 0x5140),
+                               hi0 = __byte_perm(vw[0][w], vw[1][w], 0x7362),
+                               lo1 = __byte_perm(vw[2][w], vw[3][w], 0x5140),
+                               hi1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+                const uint32_t f0[4] = {e4m3x2(lo0, false), e4m3x2(lo0, true), e4m3x2(lo1, false),
+                                        e4m3x2(lo1, true)};
+                const uint32_t f1[4] = {e4m3x2(hi0, false), e4m3x2(hi0, true), e4m3x2(hi1, false),
+                                        e4m3x2(hi1, true)};
+                if (near) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[4 * w + j][e] = fmaf(vs[1], sum[j][e], o[4 * w + j][e]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(o[n][2 * w], f0, pf[n][0], pf[n][1]);
+                        mma_f16(o[n][2 * w + 1], f1, pf[n][0], pf[n][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float own[2][4];
+                        mma_f16_from0(own[0], f0, pf[n][0], pf[n][1]);
+                        mma_f16_from0(own[1], f1, pf[n][0], pf[n][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[n][2 * w][e] = fmaf(ratio, own[0][e], o[n][2 * w][e]);
+                            o[n][2 * w + 1][e] = fmaf(ratio, own[1][e], o[n][2 * w + 1][e]);
+                        }
+                    }
+                }
+            }
         }
-        load(s + C::STAGES);
-        if ((s & 15) == 15) {  // the next 16 steps
+        if ((s & 31) == 31) {  // the next 32 steps
             ++batch;
             page_a = page_b, ks_a = ks_b, vs_a = vs_b;
             page_b = -1;
-            if ((batch + 1) * 16 < nsteps) look_up(batch + 1, page_b, ks_b, vs_b);
+            if ((batch + 1) * 32 < nsteps) look_up(batch + 1, page_b, ks_b, vs_b);
         }
     }
     cp_async_wait<0>();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
     // ------------------------------------------------- the four warps' join
     __syncthreads();  // every warp is done with its ring
-    constexpr int LD = D + 4;
-    float* so = reinterpret_cast<float*>(smem_raw);                        // (warp, row, feature)
-    float2* sml = reinterpret_cast<float2*>(smem_raw + 4 * 16 * LD * 4);   // (warp, row)
+    constexpr int LD = C::LD;
+    float* so = reinterpret_cast<float*>(smem_raw);                          // (warp, row, feature)
+    float2* sml = reinterpret_cast<float2*>(smem_raw + 4 * ROWS * LD * 4);   // (warp, row)
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            so[(warp * 16 + g + 8 * (e >> 1)) * LD + (2 * t4 + (e & 1)) * (D / 8) + j] = o[j][e];
-    if (t4 == 0) {
-        sml[warp * 16 + g] = make_float2(m[0], l[0]);
-        sml[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float* dst = so + (warp * ROWS + n * 8 + 2 * t4 + i) * LD + g * (D / 8) + 2 * j;
+                *reinterpret_cast<float2*>(dst) = make_float2(o[n][j][i] * unit, o[n][j][i + 2] * unit);
+            }
+        if (g == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                sml[warp * ROWS + n * 8 + 2 * t4 + i] = make_float2(m[n][i], l[n][i]);
+        }
     }
     __syncthreads();
-    const int r = threadIdx.x >> 3, c0 = threadIdx.x & 7;  // eight threads a row
-    if (mt * 16 + r >= rows) return;
+    constexpr int PER = 128 / ROWS;  // threads a row
+    const int r = threadIdx.x / PER, c0 = threadIdx.x % PER;
+    if (mt * ROWS + r >= rows) return;
     float mm = -INFINITY, ll = 0.f, f[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sml[w * 16 + r].x);
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sml[w * ROWS + r].x);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        const float2 ml = sml[w * 16 + r];
+        const float2 ml = sml[w * ROWS + r];
         f[w] = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
         ll += f[w] * ml.y;
     }
-    const int rr = mt * 16 + r;
+    const int rr = mt * ROWS + r;
     const size_t row = (static_cast<size_t>(b) * p.Hq + hk * G + rr % G) * p.T + rr / G;
+    // both o and the sums carry P's storage factor: it leaves with the division,
+    // and is taken out of the sum for the logarithm
     const float inv = whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-        const int c = (c0 + 8 * k) * 4;
+    for (int c = c0 * 4; c < D; c += PER * 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float4 a = *reinterpret_cast<const float4*>(so + (w * 16 + r) * LD + c);
+            const float4 a = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * LD + c);
             v.x = fmaf(f[w], a.x, v.x), v.y = fmaf(f[w], a.y, v.y);
             v.z = fmaf(f[w], a.z, v.z), v.w = fmaf(f[w], a.w, v.w);
         }
@@ -557,9 +601,9 @@ __global__ void __launch_bounds__(128, D == 128 ? 3 : 4) cache_attend_kernel(con
     }
     if (c0 == 0) {
         if (whole)
-            p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            p.lse[row] = ll > 0.f ? (mm + (log2f(ll) - kUp)) * 0.6931471805599453f : -INFINITY;
         else
-            p.part_ml[row * p.nsplit + split] = make_float2(mm, ll);
+            p.part_ml[row * p.nsplit + split] = make_float2(mm - kUp, ll);
     }
 }
 
@@ -599,21 +643,27 @@ __global__ void __launch_bounds__(128) cache_attend_join_kernel(const AttendPara
     if (lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Rows of a CTA: 8, or 16 when there are more than 8 (the codes' conversion is
+// then shared by two fragments of rows).
+inline int attend_rows(int Hq, int Hkv, int T) { return Hq / Hkv * T > 8 ? 16 : 8; }
+inline int attend_mtiles(int Hq, int Hkv, int T) {
+    const int rows = attend_rows(Hq, Hkv, T);
+    return (Hq / Hkv * T + rows - 1) / rows;
+}
+
 // Splits of a call whose sequences hold at most max_len tokens: enough CTAs to
 // fill the device's 148 multiprocessors several times over (uneven lengths even
 // out), but no split below 256 tokens, where joining costs more than it gives.
 inline void attend_splits(int B, int Hkv, int mtiles, int max_len, int* nsplit, int* split) {
     if (max_len > (1 << 30)) max_len = 1 << 30;  // split * nsplit stays an int
     const long long base = 1LL * B * Hkv * mtiles;
-    const long long want = (148 * 3 * 4 + base - 1) / base;  // splits for about four rounds of CTAs
+    const long long want = (148 * 4 * 4 + base - 1) / base;  // splits for about four rounds of CTAs
     long long len = (max_len + want - 1) / want;
-    len = (len + 127) / 128 * 128;
+    len = (len + 63) / 64 * 64;
     if (len < 256) len = 256;
     *nsplit = static_cast<int>((max_len + len - 1) / len);
     *split = static_cast<int>(len);
 }
-
-inline int attend_mtiles(int Hq, int Hkv, int T) { return (Hq / Hkv * T + 15) / 16; }
 
 inline size_t attend_workspace(int B, int Hq, int Hkv, int T, int D, int max_len) {
     int nsplit, split;
@@ -623,14 +673,19 @@ inline size_t attend_workspace(int B, int Hq, int Hkv, int T, int D, int max_len
 
 template <int D, bool BF16>
 bool attend_set_attributes() {
-    return cudaFuncSetAttribute(cache_attend_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(AttendCfg<D>::SMEM)) == cudaSuccess;
+    return cudaFuncSetAttribute(cache_attend_kernel<D, BF16, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(AttendCfg<D, 1>::SMEM)) == cudaSuccess &&
+           cudaFuncSetAttribute(cache_attend_kernel<D, BF16, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(AttendCfg<D, 2>::SMEM)) == cudaSuccess;
 }
 
 template <int D, bool BF16>
 void attend_launch(const AttendParams& p, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(p.mtiles) * p.nsplit * p.Hkv * p.B;
-    cache_attend_kernel<D, BF16><<<grid, 128, AttendCfg<D>::SMEM, st>>>(p);
+    if (attend_rows(p.Hq, p.Hkv, p.T) == 8)
+        cache_attend_kernel<D, BF16, 1><<<grid, 128, AttendCfg<D, 1>::SMEM, st>>>(p);
+    else
+        cache_attend_kernel<D, BF16, 2><<<grid, 128, AttendCfg<D, 2>::SMEM, st>>>(p);
     if (p.nsplit > 1) {
         const long long rows = 1LL * p.B * p.Hq * p.T;
         cache_attend_join_kernel<D, BF16><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
