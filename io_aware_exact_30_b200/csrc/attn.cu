@@ -1087,10 +1087,10 @@ extern "C" int attn_decay_step(const void* q, const void* k, const void* v, cons
     if (rc) return rc;
     if (!on_device(log_decay, dev)) return ATTN_ERR_DEVICE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned g = static_cast<unsigned>(B * H);
     const bool bf = dtype == ATTN_BF16;
-#define STEP_LAUNCH(D_, BF_) \
-    attn::decay_step_kernel<D_, BF_><<<g, D_, 0, st>>>(q, k, v, log_decay, state_in, state_out, o, H, scale)
+#define STEP_LAUNCH(D_, BF_)                                                                   \
+    attn::decay_step_kernel<D_, BF_, 8><<<static_cast<unsigned>(B * H) * (D_ / 32), 256, 0, st>>>( \
+        q, k, v, log_decay, state_in, state_out, o, H, scale)
     if (d == 64)
         bf ? STEP_LAUNCH(64, true) : STEP_LAUNCH(64, false);
     else

@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) cache_attend_kernel(cons
         }
     }
     cp_async_wait<0>();
+    cudaTriggerProgrammaticLaunchCompletion();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -607,19 +608,25 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) cache_attend_kernel(cons
     }
 }
 
-// Joins the splits of a row: one warp a row, lane l holding D / 32 features.
+// Joins the splits of a row: one CTA a row, its warps taking splits in turn, lane l
+// holding D / 32 features; the warps' sums meet in shared memory.  It is launched
+// while the splits still run (programmatic dependent launch) and waits for them
+// before it reads what they wrote.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) cache_attend_join_kernel(const AttendParams p) {
-    constexpr int E = D / 32;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= static_cast<long long>(p.B) * p.Hq * p.T) return;
+__global__ void __launch_bounds__(256) cache_attend_join_kernel(const AttendParams p) {
+    constexpr int E = D / 32, W = 8;
+    __shared__ float so[W][D];
+    __shared__ float sl[W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = blockIdx.x;
     const int t = static_cast<int>(row % p.T), b = static_cast<int>(row / p.T / p.Hq);
     int len, tb;
-    attend_lengths(p, b, &len, &tb, false);
-    if (t >= tb || len <= p.split) return;  // no such query, or one split: stored already
+    attend_lengths(p, b, &len, &tb, false);  // inputs of both kernels
+    cudaGridDependencySynchronize();         // every CTA: none ends before the splits have
+    if (t >= tb || len <= p.split) return;   // no such query, or one split: stored already
     const int n = min(p.nsplit, (len + p.split - 1) / p.split);
     const float2* ml = p.part_ml + row * p.nsplit;
+    const float* part = p.part + row * p.nsplit * D + lane * E;
     float mm = -INFINITY;
     for (int i = lane; i < n; i += 32) mm = fmaxf(mm, ml[i].x);
 #pragma unroll
@@ -627,20 +634,37 @@ __global__ void __launch_bounds__(128) cache_attend_join_kernel(const AttendPara
     float acc[E], ll = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+#pragma unroll 8
+    for (int i = warp; i < n; i += W) {
         const float2 v = ml[i];
         const float w = v.x == -INFINITY ? 0.f : ex2(v.x - mm);
         ll = fmaf(w, v.y, ll);
-        const float* src = p.part + (row * p.nsplit + i) * D + lane * E;
+        float x[E];
+        if constexpr (E == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(part + static_cast<size_t>(i) * D);
+            x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+            const float2 f = *reinterpret_cast<const float2*>(part + static_cast<size_t>(i) * D);
+            x[0] = f.x, x[1] = f.y;
+        }
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    if (lane == 0) sl[warp] = ll;
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    float2 v = make_float2(0.f, 0.f);
+    ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        v.x += so[w][2 * threadIdx.x], v.y += so[w][2 * threadIdx.x + 1];
+        ll += sl[w];
     }
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(p.o + (row * D + lane * E + e) * 2) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    reinterpret_cast<uint32_t*>(p.o)[row * (D / 2) + threadIdx.x] = pack2<BF16>(v.x * inv, v.y * inv);
+    if (threadIdx.x == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Rows of a CTA: 8, or 16 when there are more than 8 (the codes' conversion is
@@ -651,16 +675,20 @@ inline int attend_mtiles(int Hq, int Hkv, int T) {
     return (Hq / Hkv * T + rows - 1) / rows;
 }
 
-// Splits of a call whose sequences hold at most max_len tokens: enough CTAs to
-// fill the device's 148 multiprocessors several times over (uneven lengths even
-// out), but no split below 256 tokens, where joining costs more than it gives.
+// Splits of a call whose sequences hold at most max_len tokens: four rounds of
+// CTAs on the device's 148 multiprocessors (uneven lengths even out), but not
+// below kLong tokens a split, then one round, but not below 256.
 inline void attend_splits(int B, int Hkv, int mtiles, int max_len, int* nsplit, int* split) {
+    constexpr long long kRound = 148 * 4, kLong = 1024, kShort = 256;
     if (max_len > (1 << 30)) max_len = 1 << 30;  // split * nsplit stays an int
-    const long long base = 1LL * B * Hkv * mtiles;
-    const long long want = (148 * 4 * 4 + base - 1) / base;  // splits for about four rounds of CTAs
-    long long len = (max_len + want - 1) / want;
+    const long long tokens = 1LL * B * Hkv * mtiles * max_len;
+    long long len = tokens / (kRound * 4);
+    if (len < kLong) {
+        len = tokens / kRound;
+        len = len > kLong ? kLong : (len < kShort ? kShort : len);
+    }
     len = (len + 63) / 64 * 64;
-    if (len < 256) len = 256;
+    if (len > (1 << 30)) len = 1 << 30;
     *nsplit = static_cast<int>((max_len + len - 1) / len);
     *split = static_cast<int>(len);
 }
@@ -687,8 +715,16 @@ void attend_launch(const AttendParams& p, cudaStream_t st) {
     else
         cache_attend_kernel<D, BF16, 2><<<grid, 128, AttendCfg<D, 2>::SMEM, st>>>(p);
     if (p.nsplit > 1) {
-        const long long rows = 1LL * p.B * p.Hq * p.T;
-        cache_attend_join_kernel<D, BF16><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hq * p.T);
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute early;
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        cudaLaunchKernelEx(&cfg, cache_attend_join_kernel<D, BF16>, p);
     }
 }
 

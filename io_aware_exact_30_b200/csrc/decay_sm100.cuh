@@ -601,30 +601,57 @@ void decay_launch(const DecayMaps& maps, const DecayParams& p, cudaStream_t st) 
     decay_chunk_kernel<D, BF16, false><<<grid, 448, bytes, st>>>(maps, p);
 }
 
-// One token: one CTA per head, thread = column of the state.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(D) decay_step_kernel(const void* q, const void* k, const void* v,
-                                                       const float* log_decay, const float* in,
-                                                       float* out, void* o, int H, float scale) {
+// One token: S <- g S + k v^T, o = scale q S, the state read and written once:
+// bound by HBM (8 D^2 bytes a head).  One CTA per head and slice of 4 COLS4
+// columns; a thread holds 4 columns of D / ROWS rows, all loaded before the first
+// is used; the ROWS partial sums of o meet in shared memory.
+template <int D, bool BF16, int COLS4>
+__global__ void __launch_bounds__(256) decay_step_kernel(const void* q, const void* k, const void* v,
+                                                         const float* log_decay, const float* in,
+                                                         float* out, void* o, int H, float scale) {
+    constexpr int ROWS = 256 / COLS4, N = D / ROWS, SLICES = D / (4 * COLS4);
     __shared__ float sq[D], sk[D];
-    const int bh = blockIdx.x, c = threadIdx.x;
-    auto at = [&](const void* m) {
-        return unpack2<BF16>(static_cast<const uint16_t*>(m)[static_cast<size_t>(bh) * D + c]).x;
-    };
-    sq[c] = at(q);
-    sk[c] = at(k);
-    const float z = at(v), g = expf(decay_log(log_decay, bh % H));
-    __syncthreads();
-    const size_t state = static_cast<size_t>(bh) * D * D;
-    float acc = 0.f;
-#pragma unroll 8
-    for (int a = 0; a < D; ++a) {
-        const float s = g * in[state + a * D + c] + sk[a] * z;
-        acc += sq[a] * s;
-        out[state + a * D + c] = s;
+    __shared__ float4 so[ROWS][COLS4];
+    const int bh = blockIdx.x / SLICES, slice = blockIdx.x % SLICES;
+    const int c = threadIdx.x % COLS4, r = threadIdx.x / COLS4, col = slice * 4 * COLS4 + 4 * c;
+    const size_t at = static_cast<size_t>(bh) * D * D + static_cast<size_t>(r) * D + col;
+    float4 s[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(in + at + i * ROWS * D));
+    if (threadIdx.x < D / 2) {
+        const size_t w = static_cast<size_t>(bh) * (D / 2) + threadIdx.x;
+        const float2 a = unpack2<BF16>(static_cast<const uint32_t*>(q)[w]);
+        const float2 b = unpack2<BF16>(static_cast<const uint32_t*>(k)[w]);
+        sq[2 * threadIdx.x] = a.x, sq[2 * threadIdx.x + 1] = a.y;
+        sk[2 * threadIdx.x] = b.x, sk[2 * threadIdx.x + 1] = b.y;
     }
-    static_cast<uint16_t*>(o)[static_cast<size_t>(bh) * D + c] =
-        static_cast<uint16_t>(pack2<BF16>(acc * scale, 0.f));
+    const uint2 zv = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(v) +
+                                                     static_cast<size_t>(bh) * D + col);
+    const float2 z0 = unpack2<BF16>(zv.x), z1 = unpack2<BF16>(zv.y);
+    const float g = expf(decay_log(log_decay, bh % H));
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float a = sk[r + i * ROWS], b = sq[r + i * ROWS];
+        s[i].x = fmaf(g, s[i].x, a * z0.x), s[i].y = fmaf(g, s[i].y, a * z0.y);
+        s[i].z = fmaf(g, s[i].z, a * z1.x), s[i].w = fmaf(g, s[i].w, a * z1.y);
+        __stcs(reinterpret_cast<float4*>(out + at + i * ROWS * D), s[i]);
+        acc.x = fmaf(b, s[i].x, acc.x), acc.y = fmaf(b, s[i].y, acc.y);
+        acc.z = fmaf(b, s[i].z, acc.z), acc.w = fmaf(b, s[i].w, acc.w);
+    }
+    so[r][c] = acc;
+    __syncthreads();
+    if (threadIdx.x < COLS4) {
+        float4 sum = so[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < ROWS; ++i) {
+            const float4 x = so[i][threadIdx.x];
+            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o) + static_cast<size_t>(bh) * D + col) =
+            make_uint2(pack2<BF16>(sum.x * scale, sum.y * scale), pack2<BF16>(sum.z * scale, sum.w * scale));
+    }
 }
 
 }  // namespace attn
