@@ -401,43 +401,72 @@ def cache_alloc(num_pages: int, Hkv: int, page: int, d: int, device="cuda") -> C
     return Cache8(*codes, *scales)
 
 
+# The token-by-token calls run for a few microseconds on the device, so their
+# marshalling counts: tensors are checked without building intermediate objects,
+# addresses are passed as integers, and the current stream is read as a handle.
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _handle(t, stream):
+    """Handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not t.is_cuda:
+        raise ValueError("tensors must be device memory")
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _alike(shape, dtype, ts, names):
+    for t, n in zip(ts, names):
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous with shape {tuple(shape)} and dtype {dtype}")
+
+
+def _optional(t, shape, dtype, name):
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor")
+
+
 def _cache_shape(cache, d, page_table, B):
     """(num_pages, Hkv, page, max_pages) of a cache whose arrays fit together."""
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.shape[3] != d or k.shape[2] not in PAGE_SIZES:
+    shape = k.shape
+    if len(shape) != 4 or shape[3] != d or shape[2] not in PAGE_SIZES:
         raise ValueError(f"cache codes must be (num_pages, Hkv, page, {d}), page one of {PAGE_SIZES}")
-    if k.dtype not in _CODES or v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError("cache codes must be float8_e4m3fn or uint8, k and v alike")
-    P, Hkv, page = k.shape[:3]
-    for s in (ks, vs):
-        if s.dtype != torch.float32 or tuple(s.shape) != (P, Hkv) or not s.is_contiguous():
-            raise ValueError("cache scales must be contiguous float32 (num_pages, Hkv) tensors")
-    if not k.is_contiguous() or not v.is_contiguous():
-        raise ValueError("cache codes must be contiguous")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+    if k.dtype not in _CODES:
+        raise ValueError("cache codes must be float8_e4m3fn or uint8")
+    _alike(shape, k.dtype, (k, v), ("cache k", "cache v"))
+    _alike(shape[:2], torch.float32, (ks, vs), ("cache k_scale", "cache v_scale"))
+    table = page_table.shape
+    if page_table.dtype is not torch.int32 or len(table) != 2 or table[0] != B \
             or not page_table.is_contiguous():
         raise ValueError(f"page_table must be a contiguous int32 ({B}, max_pages) tensor")
-    return P, Hkv, page, page_table.shape[1]
+    return shape[0], shape[1], shape[2], table[1]
 
 
-def _check_lens(t, B, name):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 ({B},) tensor")
+def _check_workspace(workspace, need):
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace needs {need} bytes")
 
 
 def attn_cache_append(k, v, cache: Cache8, page_table, lens, n_new=None, stream=None) -> None:
     """Stores the first n_new[b] (None: all T) new tokens of k, v (B, Hkv, T, d)
     behind the lens[b] tokens that sequence b holds; lens is not updated."""
-    B, H, T, d = _shape(k)
-    _same(k, k, v, names=("k", "v"))
+    shape = _shape(k)
+    B, H, T, d = shape
+    code = _dtype(k)
+    _alike(shape, k.dtype, (k, v), ("k", "v"))
     P, Hkv, page, width = _cache_shape(cache, d, page_table, B)
     if H != Hkv:
         raise ValueError(f"k and v have {H} heads, the cache {Hkv}")
-    _check_lens(lens, B, "lens")
-    _check_lens(n_new, B, "n_new")
-    rc = lib().attn_cache_append(_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(page_table), _ptr(lens),
-                                 _ptr(n_new), B, H, T, d, P, page, width, _dtype(k),
-                                 ctypes.c_void_p(_stream(k.device, stream)))
+    _alike((B,), torch.int32, (lens,), ("lens",))
+    _optional(n_new, (B,), torch.int32, "n_new")
+    rc = lib().attn_cache_append(k.data_ptr(), v.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
+                                 cache[2].data_ptr(), cache[3].data_ptr(), page_table.data_ptr(),
+                                 lens.data_ptr(), _at(n_new), B, H, T, d, P, page, width, code,
+                                 _handle(k, stream))
     _check(rc, "attn_cache_append")
 
 
@@ -451,61 +480,55 @@ def attn_cache_attend(q, cache: Cache8, page_table, lens, o, lse, workspace=None
     """O, LSE <- attention of the last q_lens[b] (None: T) queries of each sequence
     over its lens[b] tokens in the cache; rows past q_lens[b] are left as they
     were.  max_len: an upper bound of lens (None: the table's capacity)."""
-    B, Hq, T, d = _shape(q)
-    _same(q, q, o, names=("q", "o"))
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 (B, Hq, T) tensor")
+    shape = _shape(q)
+    _alike(shape, q.dtype, (q, o), ("q", "o"))
+    _alike(shape[:3], torch.float32, (lse,), ("lse",))
+    _attend(q, shape, cache, page_table, lens, o, lse, workspace, causal, scale, q_lens, max_len, stream)
+
+
+def _attend(q, shape, cache, page_table, lens, o, lse, workspace, causal, scale, q_lens, max_len, stream):
+    """attn_cache_attend with o and lse known to fit; workspace False: allocate it."""
+    B, Hq, T, d = shape
+    code = _dtype(q)
     P, Hkv, page, width = _cache_shape(cache, d, page_table, B)
-    _check_lens(lens, B, "lens")
-    _check_lens(q_lens, B, "q_lens")
+    _alike((B,), torch.int32, (lens,), ("lens",))
+    _optional(q_lens, (B,), torch.int32, "q_lens")
     max_len = width * page if max_len is None else int(max_len)
-    need = attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        raise ValueError(f"workspace needs {need} bytes")
+    need = lib().attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len)
+    if workspace is False:
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
+    else:
+        _check_workspace(workspace, need)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = lib().attn_cache_attend(_ptr(q), *map(_ptr, cache), _ptr(page_table), _ptr(lens), _ptr(q_lens),
-                                 _ptr(o), _ptr(lse), _ptr(workspace), B, Hq, Hkv, T, d, P, page,
-                                 width, max_len, int(bool(causal)), scale, _dtype(q),
-                                 ctypes.c_void_p(_stream(q.device, stream)))
+    rc = _lib.attn_cache_attend(q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
+                                cache[2].data_ptr(), cache[3].data_ptr(), page_table.data_ptr(),
+                                lens.data_ptr(), _at(q_lens), o.data_ptr(), lse.data_ptr(),
+                                _at(workspace), B, Hq, Hkv, T, d, P, page, width, max_len,
+                                1 if causal else 0, scale, code, _handle(q, stream))
     _check(rc, "attn_cache_attend")
-
-
-def _check_state(t, q, name):
-    B, H, _, d = q.shape
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, H, d, d)
-                          or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 ({B}, {H}, {d}, {d}) tensor")
-
-
-def _check_decay(log_decay, H):
-    if log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (H,) or not log_decay.is_contiguous():
-        raise ValueError(f"log_decay must be a contiguous float32 ({H},) tensor")
 
 
 def attn_decay_workspace_bytes(B: int, H: int, N: int, d: int, backward: bool = False) -> int:
     return int(lib().attn_decay_workspace_bytes(B, H, N, d, int(bool(backward))))
 
 
-def _check_workspace(workspace, need):
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        raise ValueError(f"workspace needs {need} bytes")
-
-
 def attn_decay_fwd(q, k, v, log_decay, o, state_in=None, state_out=None, lens=None, workspace=None,
                    scale: float | None = None, stream=None) -> None:
     """O, state_out <- linear attention with a decay for each head, from state_in
     (None: zeros); rows of o past lens[b] are left as they were."""
-    B, H, N, d = _shape(q)
-    _same(q, q, k, v, o, names=("q", "k", "v", "o"))
-    _check_decay(log_decay, H)
-    _check_state(state_in, q, "state_in")
-    _check_state(state_out, q, "state_out")
-    _check_lens(lens, B, "lens")
-    _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d, False))
+    shape = _shape(q)
+    B, H, N, d = shape
+    code = _dtype(q)
+    _alike(shape, q.dtype, (q, k, v, o), ("q", "k", "v", "o"))
+    _alike((H,), torch.float32, (log_decay,), ("log_decay",))
+    _optional(state_in, (B, H, d, d), torch.float32, "state_in")
+    _optional(state_out, (B, H, d, d), torch.float32, "state_out")
+    _optional(lens, (B,), torch.int32, "lens")
+    _check_workspace(workspace, lib().attn_decay_workspace_bytes(B, H, N, d, 0))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = lib().attn_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_in), _ptr(lens),
-                              _ptr(o), _ptr(state_out), _ptr(workspace), B, H, N, d, scale, _dtype(q),
-                              ctypes.c_void_p(_stream(q.device, stream)))
+    rc = _lib.attn_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _at(state_in),
+                             _at(lens), o.data_ptr(), _at(state_out), _at(workspace), B, H, N, d, scale,
+                             code, _handle(q, stream))
     _check(rc, "attn_decay_fwd")
 
 
@@ -514,35 +537,39 @@ def attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state_in=None, dstate_o
                    stream=None) -> None:
     """dQ, dK, dV, dstate_in <- gradients of sum(O * dout) + sum(state_out *
     dstate_out); rows past lens[b] are left as they were."""
-    B, H, N, d = _shape(q)
-    _same(q, q, k, v, dout, dq, dk, dv, names=("q", "k", "v", "dout", "dq", "dk", "dv"))
-    _check_decay(log_decay, H)
-    for t, n in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
-        _check_state(t, q, n)
-    _check_lens(lens, B, "lens")
-    _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d, True))
+    shape = _shape(q)
+    B, H, N, d = shape
+    code = _dtype(q)
+    _alike(shape, q.dtype, (q, k, v, dout, dq, dk, dv), ("q", "k", "v", "dout", "dq", "dk", "dv"))
+    _alike((H,), torch.float32, (log_decay,), ("log_decay",))
+    _optional(state_in, (B, H, d, d), torch.float32, "state_in")
+    _optional(dstate_out, (B, H, d, d), torch.float32, "dstate_out")
+    _optional(dstate_in, (B, H, d, d), torch.float32, "dstate_in")
+    _optional(lens, (B,), torch.int32, "lens")
+    _check_workspace(workspace, lib().attn_decay_workspace_bytes(B, H, N, d, 1))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = lib().attn_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dout), _ptr(state_in),
-                              _ptr(dstate_out), _ptr(lens), _ptr(dq), _ptr(dk), _ptr(dv),
-                              _ptr(dstate_in), _ptr(workspace), B, H, N, d, scale, _dtype(q),
-                              ctypes.c_void_p(_stream(q.device, stream)))
+    rc = _lib.attn_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                             dout.data_ptr(), _at(state_in), _at(dstate_out), _at(lens), dq.data_ptr(),
+                             dk.data_ptr(), dv.data_ptr(), _at(dstate_in), _at(workspace), B, H, N, d,
+                             scale, code, _handle(q, stream))
     _check(rc, "attn_decay_bwd")
 
 
 def attn_decay_step(q, k, v, log_decay, state_in, o, state_out, scale: float | None = None,
                     stream=None) -> None:
     """O, state_out <- one token, q, k, v, o (B, H, 1, d); state_out may be state_in."""
-    B, H, N, d = _shape(q)
+    shape = _shape(q)
+    B, H, N, d = shape
     if N != 1:
         raise ValueError("a step takes one token: q must be (B, H, 1, d)")
-    _same(q, q, k, v, o, names=("q", "k", "v", "o"))
-    _check_decay(log_decay, H)
-    _check_state(state_in, q, "state_in")
-    _check_state(state_out, q, "state_out")
+    code = _dtype(q)
+    _alike(shape, q.dtype, (q, k, v, o), ("q", "k", "v", "o"))
+    _alike((H,), torch.float32, (log_decay,), ("log_decay",))
+    _alike((B, H, d, d), torch.float32, (state_in, state_out), ("state_in", "state_out"))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = lib().attn_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_in), _ptr(o),
-                               _ptr(state_out), B, H, d, scale, _dtype(q),
-                               ctypes.c_void_p(_stream(q.device, stream)))
+    rc = lib().attn_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                               state_in.data_ptr(), o.data_ptr(), state_out.data_ptr(), B, H, d, scale,
+                               code, _handle(q, stream))
     _check(rc, "attn_decay_step")
 
 
@@ -682,15 +709,13 @@ def cache_attend(q, cache: Cache8, page_table, lens, causal: bool = True, scale:
                  q_lens=None, max_len: int | None = None):
     """Allocates O, LSE and the workspace and runs attn_cache_attend; returns
     (o, lse).  Rows past q_lens[b] are 0 and -inf."""
-    B, Hq, T, d = _shape(q)
+    shape = _shape(q)
+    _alike(shape, q.dtype, (q,), ("q",))
     o = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
-    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    lse = q.new_empty(shape[:3], dtype=torch.float32)
     if q_lens is not None:
         lse.fill_(-math.inf)
-    cap = page_table.shape[1] * cache.k.shape[2] if max_len is None else int(max_len)
-    need = attn_cache_attend_workspace_bytes(B, Hq, cache.k.shape[1], T, d, cap)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    attn_cache_attend(q, cache, page_table, lens, o, lse, ws, causal, scale, q_lens, cap)
+    _attend(q, shape, cache, page_table, lens, o, lse, False, causal, scale, q_lens, max_len, None)
     return o, lse
 
 
@@ -699,9 +724,9 @@ def decay_forward(q, k, v, log_decay, scale: float | None = None, state=None, le
     (o, state after the last token).  Rows past lens[b] are 0."""
     B, H, N, d = _shape(q)
     o = torch.empty_like(q) if lens is None else torch.zeros_like(q)
-    out = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-    need = attn_decay_workspace_bytes(B, H, N, d, False)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    out = q.new_empty((B, H, d, d), dtype=torch.float32)
+    need = lib().attn_decay_workspace_bytes(B, H, N, d, 0)
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
     attn_decay_fwd(q, k, v, log_decay, o, state, out, lens, ws, scale)
     return o, out
 
@@ -712,11 +737,13 @@ def decay_backward(q, k, v, log_decay, dout, scale: float | None = None, state=N
     (dq, dk, dv, gradient of the state before the first token).  Rows past
     lens[b] are 0."""
     B, H, N, d = _shape(q)
-    new = torch.empty_like if lens is None else torch.zeros_like
-    dq, dk, dv = new(q), new(k), new(v)
-    ds = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-    need = attn_decay_workspace_bytes(B, H, N, d, True)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    if lens is None:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    else:
+        dq, dk, dv = q.new_zeros((3, B, H, N, d)).unbind()
+    ds = q.new_empty((B, H, d, d), dtype=torch.float32)
+    need = lib().attn_decay_workspace_bytes(B, H, N, d, 1)
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
     attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state, dstate, ds, lens, ws, scale)
     return dq, dk, dv, ds
 
