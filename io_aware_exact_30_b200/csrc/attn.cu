@@ -1007,12 +1007,13 @@ int check_decay(const void* const* required, int nr, const void* const* optional
     return ATTN_OK;
 }
 
+// tensors: nt inputs and results, in the order that the passes name them.
 int launch_decay(const void* const* tensors, int nt, attn::DecayParams& p, int d, int dtype,
                  void* workspace, cudaStream_t st) {
     const int BH = p.B * p.H;
     attn::DecayMaps maps;
-    for (int i = 0; i < 4; ++i)
-        if (!make_map(&maps.m[i], tensors[i < nt ? i : 0], dtype, BH, p.N, d)) return ATTN_ERR_LAUNCH;
+    for (int i = 0; i < nt; ++i)
+        if (!make_map(&maps.m[i], tensors[i], dtype, BH, p.N, d)) return ATTN_ERR_LAUNCH;
     attn::decay_segments(p.B, p.H, p.N, d, p.passes, &p.nseg, &p.seg_chunks);
     if (p.nseg > 1 && !workspace) return ATTN_ERR_NULL;
     if (1LL * BH * (d / 64) * p.passes * p.nseg >= (1LL << 31) || BH > 65535 * (p.nseg > 1 ? 1 : 32768))
@@ -1046,10 +1047,10 @@ extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const
     if (rc) return rc;
     if (!on_device(log_decay, dev) || (lens && !on_device(lens, dev))) return ATTN_ERR_DEVICE;
     attn::DecayParams p{};
-    p.pass[0] = {0, 1, 2, o, state_in, state_out, 0, 0};
+    p.pass[0] = {0, 1, 2, 3, o, state_in, state_out, 0, 0};
     p.log_decay = log_decay, p.lens = lens;
     p.passes = 1, p.B = B, p.H = H, p.N = N, p.scale = scale;
-    return launch_decay(req, 3, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
+    return launch_decay(req, 4, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -1067,13 +1068,13 @@ extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const
     if (rc) return rc;
     if (!on_device(log_decay, dev) || (lens && !on_device(lens, dev))) return ATTN_ERR_DEVICE;
     attn::DecayParams p{};
-    // tensors 0 q, 1 k, 2 v, 3 dout
-    p.pass[0] = {3, 2, 1, dq, state_in, nullptr, 1, 0};
-    p.pass[1] = {2, 3, 0, dk, dstate_out, nullptr, 1, 1};
-    p.pass[2] = {1, 0, 3, dv, dstate_out, dstate_in, 0, 1};
+    // tensors 0 q, 1 k, 2 v, 3 dout, 4 dq, 5 dk, 6 dv
+    p.pass[0] = {3, 2, 1, 4, dq, state_in, nullptr, 1, 0};
+    p.pass[1] = {2, 3, 0, 5, dk, dstate_out, nullptr, 1, 1};
+    p.pass[2] = {1, 0, 3, 6, dv, dstate_out, dstate_in, 0, 1};
     p.log_decay = log_decay, p.lens = lens;
     p.passes = 3, p.B = B, p.H = H, p.N = N, p.scale = scale;
-    return launch_decay(req, 4, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
+    return launch_decay(req, 7, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int attn_decay_step(const void* q, const void* k, const void* v, const float* log_decay,

@@ -21,6 +21,7 @@ namespace attn {
 // One pass of the operator over x_t (in place of q), y_t (k) and z_t (v).
 struct DecayPass {
     int x, y, z;         // which of the tensor maps
+    int out_map;         // and the result's
     void* out;           // (B, H, N, D)
     const float* init;   // (B, H, D, D) or null: the state before the first token
     float* last;         // (B, H, D, D) or null: the state after the last token
@@ -49,7 +50,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 struct DecayMaps {
-    CUtensorMap m[4];
+    CUtensorMap m[7];
 };
 
 __device__ __forceinline__ int decay_len(const int* lens, int b, int N) {
@@ -96,14 +97,20 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // 768, X S and P Z 380 cycles each against 1300 for the chunk's share of HBM
 // bandwidth), by HBM at D = 64.
 //
-// Roles (448 threads): warp 0 loads (TMA), warp 1 issues the products, warps 2-9
-// make P and the output (thread = token; warps 2-5 keys 0-63 of P and features
-// 0-31, warps 6-9 the rest), warps 10-13 hold the state (thread = feature of y)
-// and make Zh (thread = token).  Issue order: A_0, then per chunk Y^T Zh, X S,
+// Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
+// products; 16 warps make P and the output (thread = token; each 32 keys of P and
+// 16 features); 4 hold the state (thread = feature of y); 8 make Zh (thread =
+// token, 32 features each).  Every role's work lies on the chain from one chunk to
+// the next (Zh is written when its last reader is done), so it is spread over as many
+// warps as the registers carry: with 8 + 4 + 4 warps the same work took XX us for the large-head
+// prompt.  Registers are dealt out
+// between the warpgroups (setmaxnreg).  Issue order: A_0, then per chunk Y^T Zh, X S,
 // A of the next chunk, P Z: while the row warps read X S and hand over P, the
-// next A runs, and the next P is made during P Z and Y^T Zh.  X, Y and Z have
-// their own barriers per stage, so each is reloaded as soon as its last product
-// is done (one barrier for the three left the loads too little time).
+// next A runs, and the next P is made during P Z and Y^T Zh.  Every product has a
+// completion barrier for either stage, on which all that depends on it waits, the
+// reload of its operand included: X, Y and Z are each reloaded as soon as their
+// last product is done, and each product is committed once.  (A second commit
+// behind the same products held the issuing thread for about 1200 cycles.)
 //
 // STATE: only the segment's own contribution to the state (from zero).
 template <int D, bool BF16>
@@ -115,20 +122,33 @@ struct DecayCfg {
     static constexpr uint32_t STAGE = XB + YB + ZB;
     static constexpr uint32_t OFF_ZH = 2 * STAGE;
     static constexpr uint32_t OFF_S = OFF_ZH + NP * ZB;  // D rows of 64 features
-    static constexpr uint32_t OFF_PW = OFF_S + D * 128u; // L^0 .. L^128, then L^31 .. L^0
-    static constexpr uint32_t OFF_BAR = OFF_PW + (132 + 32) * 4;
-    static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_XE = 6, B_YE = 8, B_ZE = 10, B_AF = 12,
-                         B_PF = 14, B_ZH = 15, B_KVF = 16, B_KVE = 17, B_SSF = 18, B_QSD = 19,
-                         B_OD = 20, B_OE = 21, B_DR = 22, NBAR = 23;
+    static constexpr uint32_t OFF_PW = OFF_S + D * 128u; // 32 zeros, L^0 .. L^128, L^31 .. L^0
+    static constexpr uint32_t OFF_BAR = OFF_PW + (32 + 132 + 32) * 4;
+    // two each of the loads and the products (by step parity), one of the rest
+    static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_AF = 6, B_KVF = 8, B_QSD = 10, B_OD = 12,
+                         B_PF = 14, B_ZH = 15, B_KVE = 16, B_SSF = 17, B_OE = 18, B_DR = 19, B_ZE = 20,
+                         B_OW = 22, NBAR = 23;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;
     static constexpr uint32_t COL_KV = 256, COL_O = 448;  // tensor memory: A at 0 and 128
-    static constexpr int NROW = 256, NSTATE = 128, NTHREADS = 448;
+    static constexpr int NROW = 512, NSTATE = 128, NZH = 256, NTHREADS = 1024;
+    // registers of a thread by role; the launch gives each of the eight warpgroups 64
+    static constexpr int R_ISSUE = 32, R_ROW = 56, R_STATE = 144, R_ZH = 56;
+    static_assert(R_ISSUE + 4 * R_ROW + R_STATE + 2 * R_ZH <= 8 * 64, "more registers than the launch has");
     static_assert(SMEM_BYTES <= 232448u, "dynamic shared memory above the sm_100 per-block limit");
 };
 
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D, bool BF16, bool STATE>
-__global__ void __launch_bounds__(448, 1)
+__global__ void __launch_bounds__(1024, 1)
     decay_chunk_kernel(const __grid_constant__ DecayMaps maps, const __grid_constant__ DecayParams p) {
     using C = DecayCfg<D, BF16>;
     constexpr int HALVES = D / 64, NP = C::NP;
@@ -158,13 +178,13 @@ __global__ void __launch_bounds__(448, 1)
 #define DBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    float* pw = reinterpret_cast<float*>(gbase + C::OFF_PW);
+    float* pw = reinterpret_cast<float*>(gbase + C::OFF_PW) + 32;
     const double ld = decay_log(p.log_decay, bh % p.H);
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
-            const int rows = i == C::B_PF || i == C::B_OE;
-            const int state = i == C::B_ZH || i == C::B_KVE || i == C::B_SSF;
-            mbar_init(DBAR(i), rows ? C::NROW : (state ? C::NSTATE : 1));
+            const int rows = i == C::B_PF || i == C::B_OE || i == C::B_OW;
+            const int state = i == C::B_KVE || i == C::B_SSF;
+            mbar_init(DBAR(i), rows ? C::NROW : (state ? C::NSTATE : (i == C::B_ZH ? C::NZH : 1)));
         }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -172,7 +192,7 @@ __global__ void __launch_bounds__(448, 1)
     // L^m by the exponential of a double product: a power's error stays one rounding
     for (int m = threadIdx.x; m <= kDecayChunk; m += C::NTHREADS) {
         pw[m] = static_cast<float>(exp(ld * m));
-        if (m < 32) pw[132 + 31 - m] = pw[m];
+        if (m < 32) pw[132 + 31 - m] = pw[m], pw[-1 - m] = 0.f;
     }
     if (D == 64) {  // features 64-127 of Y: zeros that no load touches
         for (int i = threadIdx.x; i < 2 * 1024; i += C::NTHREADS)
@@ -188,6 +208,7 @@ __global__ void __launch_bounds__(448, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (warp < 4) regs_down<C::R_ISSUE>();
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (elect_one()) {
@@ -198,21 +219,21 @@ __global__ void __launch_bounds__(448, 1)
                 const int s = i & 1, row = chunk(i) * kDecayChunk;
                 const uint32_t par = ((i >> 1) - 1) & 1;
                 const uint32_t sx = base + s * C::STAGE, sy = sx + C::XB, sz = sy + C::YB;
-                if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_YE + s), par, abort_flag))) break;
+                if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_KVF + s), par, abort_flag))) break;
                 mbar_arrive_expect_tx(DBAR(C::B_YF + s), D * 256u);
 #pragma unroll
                 for (int kb = 0; kb < HALVES; ++kb)
                     tma_load_3d(sy + kb * 16384u, my, DBAR(C::B_YF + s), kb * 64, row, bh);
                 issued = 3 * i + 1;
                 if constexpr (!STATE) {
-                    if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_XE + s), par, abort_flag))) break;
+                    if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_QSD + s), par, abort_flag))) break;
                     mbar_arrive_expect_tx(DBAR(C::B_XF + s), D * 256u);
 #pragma unroll
                     for (int kb = 0; kb < HALVES; ++kb)
                         tma_load_3d(sx + kb * 16384u, mx, DBAR(C::B_XF + s), kb * 64, row, bh);
                 }
                 issued = 3 * i + 2;
-                if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_ZE + s), par, abort_flag))) break;
+                if (!STATE && i >= 2 && !(ok = wait_bounded(DBAR(C::B_ZE + s), par, abort_flag))) break;
                 mbar_arrive_expect_tx(DBAR(C::B_ZF + s), C::ZB);
                 tma_load_3d(sz, mz, DBAR(C::B_ZF + s), hf * 64, row, bh);
                 issued = 3 * i + 3;
@@ -234,9 +255,9 @@ __global__ void __launch_bounds__(448, 1)
             constexpr uint32_t ID_O = idesc_f16(BF16, 128, 64, false, true);       // X S, P Z
             // descriptors of X and, transposed, of Y and Z of either stage, of Zh and of
             // the state's copy; a step along them is an addition to the address
-            const uint64_t dx[2] = {sdesc_sw128(base, 16, 1024), sdesc_sw128(base + C::STAGE, 16, 1024)};
-            const uint64_t dy[2] = {sdesc_sw128(base + C::XB, 16384, 1024),
-                                    sdesc_sw128(base + C::STAGE + C::XB, 16384, 1024)};
+            // (no arrays of them: indexed by the stage they would live in local memory)
+            const uint64_t dx = sdesc_sw128(base, 16, 1024), dy = sdesc_sw128(base + C::XB, 16384, 1024);
+            constexpr uint32_t ST16 = C::STAGE >> 4;
             const uint64_t dzh = sdesc_sw128(base + C::OFF_ZH, 16384, 1024);
             const uint64_t dst = sdesc_sw128(base + C::OFF_S, 16384, 1024);
             // A of step i into its buffer, last read by the P Z of step i - 2; in
@@ -244,11 +265,11 @@ __global__ void __launch_bounds__(448, 1)
             auto issue_a = [&](int i) -> bool {
                 const int s = i & 1;
                 if (!wait3(DBAR(C::B_XF + s), (i >> 1) & 1, true, DBAR(C::B_YF + s), (i >> 1) & 1, true,
-                           DBAR(C::B_OD), i & 1, i >= 2, abort_flag))
+                           DBAR(C::B_OD + s), ((i >> 1) - 1) & 1, i >= 2, abort_flag))
                     return false;
                 if (tokens(i) < kDecayChunk && !wait_bounded(DBAR(C::B_ZH), i & 1, abort_flag)) return false;
                 tc_fence_after();
-                const uint64_t x = dx[s], y = x + (C::XB >> 4);
+                const uint64_t x = dx + s * ST16, y = x + (C::XB >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
@@ -268,12 +289,9 @@ __global__ void __launch_bounds__(448, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)  // 16 tokens (2048 bytes) per step
-                    mma_ss(tmem + C::COL_KV, dy[s] + kk * 128u, dzh + kk * 128u, ID_KV, kk > 0 ? 1u : 0u);
-                mma_commit(DBAR(C::B_KVF));
-                mma_commit(DBAR(C::B_YE + s));
-                if constexpr (STATE) {
-                    mma_commit(DBAR(C::B_ZE + s));
-                } else {
+                    mma_ss(tmem + C::COL_KV, dy + s * ST16 + kk * 128u, dzh + kk * 128u, ID_KV, kk > 0 ? 1u : 0u);
+                mma_commit(DBAR(C::B_KVF + s));
+                if constexpr (!STATE) {
                     // the state's copy stored, the previous output read
                     if (!(ok = wait3(DBAR(C::B_SSF), i & 1, true, DBAR(C::B_OE), (i - 1) & 1, i >= 1, 0u, 0u,
                                      false, abort_flag)))
@@ -282,20 +300,18 @@ __global__ void __launch_bounds__(448, 1)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
-                        mma_ss(tmem + C::COL_O, dx[s] + off, dst + kk * 128u, ID_O, kk > 0 ? 1u : 0u);
+                        mma_ss(tmem + C::COL_O, dx + s * ST16 + off, dst + kk * 128u, ID_O, kk > 0 ? 1u : 0u);
                     }
-                    mma_commit(DBAR(C::B_QSD));
-                    mma_commit(DBAR(C::B_XE + s));
+                    mma_commit(DBAR(C::B_QSD + s));
                     if (i + 1 < nch && !(ok = issue_a(i + 1))) break;
                     // P written and X S read: P Z takes its columns
                     if (!(ok = wait_bounded(DBAR(C::B_PF), i & 1, abort_flag))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + C::COL_O, tmem + 128u * s + kk * 8u + (kk >> 2) * 32u,
-                               dy[s] + (C::YB >> 4) + kk * 128u, ID_O, kk > 0 ? 1u : 0u);
-                    mma_commit(DBAR(C::B_OD));
-                    mma_commit(DBAR(C::B_ZE + s));
+                        mma_ts(tmem + C::COL_O, tmem + 128u * s + (kk >> 1) * 32u + (kk & 1) * 8u,
+                               dy + s * ST16 + (C::YB >> 4) + kk * 128u, ID_O, kk > 0 ? 1u : 0u);
+                    mma_commit(DBAR(C::B_OD + s));
                 }
             }
             if (!ok) {  // every issued MMA must finish before tensor memory is freed
@@ -304,9 +320,29 @@ __global__ void __launch_bounds__(448, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 10) {
+    } else if (warp == 2) {
+        // ---------------------------------------------------------- output
+        // O_i, staged in the stage of Z_i, leaves by TMA; the stage is then free
+        if (!STATE && elect_one()) {
+            for (int i = 0; i < nch; ++i) {
+                const int s = i & 1;
+                if (!wait_bounded(DBAR(C::B_OW), i & 1, abort_flag)) break;
+                if (tokens(i) == kDecayChunk) {
+                    tma_store_3d(&maps.m[ps.out_map], base + s * C::STAGE + C::XB + C::YB, hf * 64,
+                                 chunk(i) * kDecayChunk, bh);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive(DBAR(C::B_ZE + s));
+            }
+            bulk_wait_all();
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+    } else if (warp < 20) {
         // ----------------------------------------- P and the output (rows)
-        const int hc = (warp - 2) >> 2;        // keys 64 hc.. of P, features 32 hc.. of O
+        regs_down<C::R_ROW>();
+        const int cb = (warp - 4) >> 2;        // keys 32 cb.. of P, features 16 cb.. of O
         const int wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float* near = rev ? pw : pw + 132;
@@ -314,100 +350,115 @@ __global__ void __launch_bounds__(448, 1)
             const int b = i & 1, n = tokens(i);
             if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_AF + b), (i >> 1) & 1, abort_flag))) break;
             tc_fence_after();
-            const uint32_t col = 128u * b + 64u * hc;
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                const int cb = hc * 2 + cc;  // 32 keys: all before, all behind or around the row's warp
+            {
+                const uint32_t col = lane_addr + 128u * b + 32u * cb;
                 uint32_t pk[16];
-                if (rev ? cb < wq : cb > wq) {
+                if (rev ? cb < wq : cb > wq) {  // 32 keys behind all rows of the warp
 #pragma unroll
                     for (int e = 0; e < 16; ++e) pk[e] = 0u;
-                    // the lower block is read before P is packed over it
                 } else {
                     uint32_t v[32];
-                    tmem_ld32(lane_addr + col + cc * 32u, v);
+                    tmem_ld32(col, v);
                     tmem_ld_wait();
                     reg_fence32(v);
                     if (cb == wq) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
+                            // (the zeros in front of L^0 keep the load unconditional: a
+                            // branch for each key made this block the whole chunk's pace)
                             const int gap = rev ? e - lane : lane - e;
-                            v[e] = gap >= 0 ? __float_as_uint(__uint_as_float(v[e]) * (pw[gap] * p.scale)) : 0u;
+                            const float x = __uint_as_float(v[e]) * (pw[gap] * p.scale);
+                            v[e] = gap >= 0 ? __float_as_uint(x) : 0u;
                         }
                     } else {
                         // L^(distance) as L^(from the row to the block's near end) times
                         // L^(from there to the key), neither above 1
                         const float u = p.scale * (rev ? pw[cb * 32 - r] : pw[r - cb * 32 - 31]);
+                        const uint64_t u2 = f2(u, u);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * (u * near[e]));
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 w = *reinterpret_cast<const float4*>(near + e);
+                            const float2 a = unf2(mul2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                                       mul2(u2, f2(w.x, w.y))));
+                            const float2 c = unf2(mul2(f2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                                                       mul2(u2, f2(w.z, w.w))));
+                            v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y);
+                            v[e + 2] = __float_as_uint(c.x), v[e + 3] = __float_as_uint(c.y);
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         pk[e] = pack2<BF16>(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                 }
-                tmem_st16(lane_addr + col + cc * 16u, pk);  // over columns already read
+                tmem_st16(col, pk);  // over columns already read
+                tmem_st_wait();
             }
-            tmem_st_wait();
-            // X S, weighted, before P Z takes its columns
-            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD), i & 1, abort_flag))) break;
+            // X S, before P Z takes its columns
+            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD + b), (i >> 1) & 1, abort_flag))) break;
             tc_fence_after();
-            uint32_t ox[32];
-            tmem_ld32(lane_addr + C::COL_O + 32u * hc, ox);
+            uint32_t ox[16], v[16];
+            tmem_ld16(lane_addr + C::COL_O + 16u * cb, ox);
             tmem_ld_wait();
-            reg_fence32(ox);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) reg_fence(ox[e]);
             tc_fence_before();
             mbar_arrive(DBAR(C::B_PF));
-            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OD), i & 1, abort_flag))) break;
+            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OD + b), (i >> 1) & 1, abort_flag))) break;
             tc_fence_after();
-            uint32_t v[32];
-            tmem_ld32(lane_addr + C::COL_O + 32u * hc, v);
+            tmem_ld16(lane_addr + C::COL_O + 16u * cb, v);
             tmem_ld_wait();
-            reg_fence32(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) reg_fence(v[e]);
             tc_fence_before();
             mbar_arrive(DBAR(C::B_OE));
-            if (r < n) {
-                const float w = rev ? pw[n - 1 - r] : pw[r + 1];
-                uint32_t o16[16];
+            const float w = r < n ? (rev ? pw[n - 1 - r] : pw[r + 1]) : 0.f;
+            uint32_t o16[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
-                                         fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
+            for (int e = 0; e < 8; ++e)
+                o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
+                                     fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
+            if (n == kDecayChunk) {
+                // into the stage of Z, which P Z has read, as the TMA store expects it
+                // (16-byte piece j of row r at j ^ (r mod 8)).  Stored from registers, 32
+                // bytes of each row by a thread, every store was 32 wavefronts of L1: 31 of
+                // the large-head prompt's 103 us.
+                uint8_t* dst = gbase + b * C::STAGE + C::XB + C::YB + r * 128;
+                *reinterpret_cast<uint4*>(dst + (((2 * cb) ^ (r & 7)) << 4)) = make_uint4(o16[0], o16[1], o16[2], o16[3]);
+                *reinterpret_cast<uint4*>(dst + (((2 * cb + 1) ^ (r & 7)) << 4)) =
+                    make_uint4(o16[4], o16[5], o16[6], o16[7]);
+                fence_proxy_async_smem();
+            } else if (r < n) {  // rows past the sequence's end stay as they are
                 uint4* dst = reinterpret_cast<uint4*>(
                     static_cast<uint8_t*>(ps.out) +
-                    (static_cast<size_t>(bh) * p.N + chunk(i) * kDecayChunk + r) * (D * 2) + hf * 128 + hc * 64);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dst[e] = make_uint4(o16[4 * e], o16[4 * e + 1], o16[4 * e + 2], o16[4 * e + 3]);
+                    (static_cast<size_t>(bh) * p.N + chunk(i) * kDecayChunk + r) * (D * 2) + hf * 128 + cb * 32);
+                dst[0] = make_uint4(o16[0], o16[1], o16[2], o16[3]);
+                dst[1] = make_uint4(o16[4], o16[5], o16[6], o16[7]);
             }
+            mbar_arrive(DBAR(C::B_OW));
         }
-    } else {
-        // ------------------------------------------------- the state and Zh
-        const int a = (warp & 3) * 32 + lane;  // feature of y == TMEM lane; token of Zh
+    } else if (warp < 24) {
+        // -------------------------------------------------------- the state
+        regs_up<C::R_STATE>();
+        const int a = (warp & 3) * 32 + lane;  // feature of y == TMEM lane
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const size_t mat = static_cast<size_t>(bh) * D * D;
         const size_t seg_mat = (static_cast<size_t>(pi) * p.nseg + seg) * p.B * p.H * D * D + mat;
-        const float zscale = rev ? p.scale : 1.f, copy = rev ? 1.f : p.scale;
-        float st[64];
+        const float copy = rev ? 1.f : p.scale;
+        uint64_t st[32];  // features 2 c, 2 c + 1 of z
 #pragma unroll
-        for (int c = 0; c < 64; ++c) st[c] = 0.f;
+        for (int c = 0; c < 32; ++c) st[c] = 0ull;
         if (!STATE && a < D) {
-            if (p.nseg > 1) {
-                const float4* src = reinterpret_cast<const float4*>(p.seg + seg_mat + a * D + hf * 64);
+            if (p.nseg == 1 && ps.init && ps.transposed) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    st[c] = f2(ps.init[mat + (hf * 64 + 2 * c) * D + a], ps.init[mat + (hf * 64 + 2 * c + 1) * D + a]);
+            } else if (p.nseg > 1 || ps.init) {
+                const float4* src = reinterpret_cast<const float4*>((p.nseg > 1 ? p.seg + seg_mat : ps.init + mat) +
+                                                                    a * D + hf * 64);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const float4 f = src[c];
-                    st[4 * c] = f.x, st[4 * c + 1] = f.y, st[4 * c + 2] = f.z, st[4 * c + 3] = f.w;
-                }
-            } else if (ps.init && ps.transposed) {
-#pragma unroll
-                for (int c = 0; c < 64; ++c) st[c] = ps.init[mat + (hf * 64 + c) * D + a];
-            } else if (ps.init) {
-                const float4* src = reinterpret_cast<const float4*>(ps.init + mat + a * D + hf * 64);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const float4 f = src[c];
-                    st[4 * c] = f.x, st[4 * c + 1] = f.y, st[4 * c + 2] = f.z, st[4 * c + 3] = f.w;
+                    st[2 * c] = f2(f.x, f.y), st[2 * c + 1] = f2(f.z, f.w);
                 }
             }
         }
@@ -416,73 +467,106 @@ __global__ void __launch_bounds__(448, 1)
         auto store_copy = [&]() {
             if (a < D) {
                 uint8_t* srow = gbase + C::OFF_S + a * 128;
+                const uint64_t c2 = f2(copy, copy);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(srow + ((j ^ (a & 7)) << 4)) =
-                        make_uint4(pack2<BF16>(st[8 * j] * copy, st[8 * j + 1] * copy),
-                                   pack2<BF16>(st[8 * j + 2] * copy, st[8 * j + 3] * copy),
-                                   pack2<BF16>(st[8 * j + 4] * copy, st[8 * j + 5] * copy),
-                                   pack2<BF16>(st[8 * j + 6] * copy, st[8 * j + 7] * copy));
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unf2(mul2(st[4 * j + e], c2));
+                        w[e] = pack2<BF16>(f.x, f.y);
+                    }
+                    *reinterpret_cast<uint4*>(srow + ((j ^ (a & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(DBAR(C::B_SSF));
         };
-        // the sums of step i (complete) into the state: S <- L^n S + sums, L^n as a
-        // pair of floats so that its error does not add up over the chunks
+        if constexpr (!STATE) store_copy();
+        bool ok = true;
         const double full = exp(ld * kDecayChunk);
-        auto add_sums = [&](int i) {
+        for (int i = 0; i < nch; ++i) {
+            // the sums of step i into the state: S <- L^n S + sums, L^n as a pair of
+            // floats so that its error does not add up over the chunks
+            if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_KVF + (i & 1)), (i >> 1) & 1, abort_flag))))
+                break;
             tc_fence_after();
             const double gd = tokens(i) == kDecayChunk ? full : exp(ld * tokens(i));
-            const float g = static_cast<float>(gd), g2 = static_cast<float>(gd - g);
+            const float gf = static_cast<float>(gd);
+            const uint64_t g = f2(gf, gf), g2 = f2(static_cast<float>(gd - gf), static_cast<float>(gd - gf));
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                uint32_t v[32];
-                float sum[32];
+            for (int cc = 0; cc < 4; ++cc) {
+                uint32_t v[NP][16];
 #pragma unroll
-                for (int k = NP - 1; k >= 0; --k) {  // the small pieces first
-                    tmem_ld32(lane_addr + C::COL_KV + 64u * k + 32u * cc, v);
-                    tmem_ld_wait();
-                    reg_fence32(v);
+                for (int k = 0; k < NP; ++k) tmem_ld16(lane_addr + C::COL_KV + 64u * k + 16u * cc, v[k]);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        sum[e] = k == NP - 1 ? __uint_as_float(v[e]) : sum[e] + __uint_as_float(v[e]);
+                for (int k = 0; k < NP; ++k)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) reg_fence(v[k][e]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint64_t sum = f2(__uint_as_float(v[NP - 1][2 * e]), __uint_as_float(v[NP - 1][2 * e + 1]));
+#pragma unroll
+                    for (int k = NP - 2; k >= 0; --k)  // the small pieces first
+                        sum = add2(sum, f2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])));
+                    uint64_t& x = st[8 * cc + e];
+                    x = fma2(g, x, fma2(g2, x, sum));
                 }
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    st[cc * 32 + e] = fmaf(g, st[cc * 32 + e], fmaf(g2, st[cc * 32 + e], sum[e]));
             }
             tc_fence_before();
             mbar_arrive(DBAR(C::B_KVE));
-        };
-        if constexpr (!STATE) store_copy();
-        bool ok = true;
+            if (!STATE && i + 1 < nch) {
+                // the copy was last read by X S of this step
+                if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD + (i & 1)), (i >> 1) & 1, abort_flag))))
+                    break;
+                store_copy();
+            }
+        }
+        float* last = STATE ? p.seg + seg_mat : (p.nseg == 1 && ps.last ? ps.last + mat : nullptr);
+        if (ok && last && a < D) {
+            float4* dst = reinterpret_cast<float4*>(last + a * D + hf * 64);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float2 f = unf2(st[2 * c]), h = unf2(st[2 * c + 1]);
+                dst[c] = make_float4(f.x, f.y, h.x, h.y);
+            }
+        }
+    } else {
+        // -------------------------------------------------------------- Zh
+        regs_down<C::R_ZH>();
+        const int a = (warp & 3) * 32 + lane;  // token
+        const int j0 = (warp - 24) >> 2 << 2;  // features 8 j0 ..
+        const float zscale = rev ? p.scale : 1.f;
         for (int i = 0; i < nch; ++i) {
             const int s = i & 1, n = tokens(i);
             // Z landed; the previous product has read Zh
-            ok = wait_bounded(DBAR(C::B_ZF + s), (i >> 1) & 1, abort_flag) &&
-                 (i == 0 || wait_bounded(DBAR(C::B_KVF), (i - 1) & 1, abort_flag));
+            bool ok = wait_bounded(DBAR(C::B_ZF + s), (i >> 1) & 1, abort_flag) &&
+                      (i == 0 || wait_bounded(DBAR(C::B_KVF + (s ^ 1)), ((i - 1) >> 1) & 1, abort_flag));
             if (n < kDecayChunk)  // Y is cleared below
                 ok = ok && wait_bounded(DBAR(C::B_YF + s), (i >> 1) & 1, abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (!__all_sync(0xffffffffu, ok)) break;
             uint8_t* zrow = gbase + s * C::STAGE + C::XB + C::YB + a * 128;
             uint8_t* hrow = gbase + C::OFF_ZH + a * 128;
             if (a < n) {
                 const float w = (rev ? pw[a + 1] : pw[n - 1 - a]) * zscale;
+                const uint64_t w2 = f2(w, w), minus = f2(-1.f, -1.f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t at = (j ^ (a & 7)) << 4;
+                for (int jj = 0; jj < 4; ++jj) {
+                    const uint32_t at = ((j0 + jj) ^ (a & 7)) << 4;
                     const uint4 in = *reinterpret_cast<const uint4*>(zrow + at);
                     const uint32_t z[4] = {in.x, in.y, in.z, in.w};
                     uint32_t out[NP][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float2 f = unpack2<BF16>(z[e]);
-                        f.x *= w, f.y *= w;
+                        const float2 zf = unpack2<BF16>(z[e]);
+                        uint64_t f = mul2(f2(zf.x, zf.y), w2);
 #pragma unroll
                         for (int k = 0; k < NP; ++k) {
-                            out[k][e] = pack2<BF16>(f.x, f.y);
-                            const float2 g = unpack2<BF16>(out[k][e]);
-                            f.x -= g.x, f.y -= g.y;
+                            const float2 x = unf2(f);
+                            out[k][e] = pack2<BF16>(x.x, x.y);
+                            const float2 h = unpack2<BF16>(out[k][e]);
+                            f = fma2(f2(h.x, h.y), minus, f);
                         }
                     }
 #pragma unroll
@@ -494,7 +578,7 @@ __global__ void __launch_bounds__(448, 1)
                 // a token past the end: it may hold anything, NaN included, in y and z
                 const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = j0; j < j0 + 4; ++j) {
                     *reinterpret_cast<uint4*>(zrow + j * 16) = none;
 #pragma unroll
                     for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4*>(hrow + k * C::ZB + j * 16) = none;
@@ -506,25 +590,6 @@ __global__ void __launch_bounds__(448, 1)
             }
             fence_proxy_async_smem();
             mbar_arrive(DBAR(C::B_ZH));
-            if (i >= 1) {
-                add_sums(i - 1);
-                if constexpr (!STATE) {
-                    // the copy was last read by X S of step i - 1
-                    ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD), (i - 1) & 1, abort_flag));
-                    if (!ok) break;
-                    store_copy();
-                }
-            }
-        }
-        if (ok && nch > 0)
-            if ((ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_KVF), (nch - 1) & 1, abort_flag))))
-                add_sums(nch - 1);
-        float* last = STATE ? p.seg + seg_mat : (p.nseg == 1 && ps.last ? ps.last + mat : nullptr);
-        if (ok && last && a < D) {
-            float4* dst = reinterpret_cast<float4*>(last + a * D + hf * 64);
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-                dst[c] = make_float4(st[4 * c], st[4 * c + 1], st[4 * c + 2], st[4 * c + 3]);
         }
     }
 #undef DBAR
@@ -608,10 +673,10 @@ void decay_launch(const DecayMaps& maps, const DecayParams& p, cudaStream_t st) 
     constexpr uint32_t bytes = DecayCfg<D, BF16>::SMEM_BYTES;
     const unsigned grid = static_cast<unsigned>(p.B) * p.H * (D / 64) * p.passes * p.nseg;
     if (p.nseg > 1) {
-        decay_chunk_kernel<D, BF16, true><<<grid, 448, bytes, st>>>(maps, p);
+        decay_chunk_kernel<D, BF16, true><<<grid, 1024, bytes, st>>>(maps, p);
         decay_scan_kernel<D><<<dim3(D * D / 1024, p.B * p.H, p.passes), 256, 0, st>>>(p);
     }
-    decay_chunk_kernel<D, BF16, false><<<grid, 448, bytes, st>>>(maps, p);
+    decay_chunk_kernel<D, BF16, false><<<grid, 1024, bytes, st>>>(maps, p);
 }
 
 // One token: S <- g S + k v^T, o = scale q S, the state read and written once:
