@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(1024, 1)
         const int wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float* near = rev ? pw : pw + 132;
+        const bool steep = pw[31] < 0x1p-100f;  // L^-31 out of range
         for (int i = 0; !STATE && i < nch; ++i) {
             const int b = i & 1, n = tokens(i);
             if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_AF + b), (i >> 1) & 1, abort_flag))) break;
@@ -361,19 +362,19 @@ __global__ void __launch_bounds__(1024, 1)
                     tmem_ld32(col, v);
                     tmem_ld_wait();
                     reg_fence32(v);
-                    if (cb == wq) {
+                    if (cb == wq && steep) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            // (the zeros in front of L^0 keep the load unconditional: a
-                            // branch for each key made this block the whole chunk's pace)
-                            const int gap = rev ? e - lane : lane - e;
+                            const int gap = rev ? e - lane : lane - e;  // zeros in front of L^0
                             const float x = __uint_as_float(v[e]) * (pw[gap] * p.scale);
                             v[e] = gap >= 0 ? __float_as_uint(x) : 0u;
                         }
                     } else {
                         // L^(distance) as L^(from the row to the block's near end) times
-                        // L^(from there to the key), neither above 1
-                        const float u = p.scale * (rev ? pw[cb * 32 - r] : pw[r - cb * 32 - 31]);
+                        // L^(from there to the key): neither above 1 behind the row, and in
+                        // the row's own block the first at most L^-31
+                        const float u = cb == wq ? p.scale / pw[rev ? lane : 31 - lane]
+                                                 : p.scale * (rev ? pw[cb * 32 - r] : pw[r - cb * 32 - 31]);
                         const uint64_t u2 = f2(u, u);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -384,6 +385,12 @@ __global__ void __launch_bounds__(1024, 1)
                                                        mul2(u2, f2(w.z, w.w))));
                             v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y);
                             v[e + 2] = __float_as_uint(c.x), v[e + 3] = __float_as_uint(c.y);
+                        }
+                        if (cb == wq) {
+                            const uint32_t seen = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen & (1u << e))) v[e] = 0u;
                         }
                     }
 #pragma unroll
