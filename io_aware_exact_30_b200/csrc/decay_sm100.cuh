@@ -189,9 +189,11 @@ __global__ void __launch_bounds__(1024, 1)
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    // L^m by the exponential of a double product: a power's error stays one rounding
+    // L^m; the product's rounding error enters as a correction, so a power's error
+    // stays that of the exponential
     for (int m = threadIdx.x; m <= kDecayChunk; m += C::NTHREADS) {
-        pw[m] = static_cast<float>(exp(ld * m));
+        const float l1 = static_cast<float>(ld), x = l1 * m;
+        pw[m] = expf(x) * (1.f + fmaf(l1, static_cast<float>(m), -x));
         if (m < 32) pw[132 + 31 - m] = pw[m], pw[-1 - m] = 0.f;
     }
     if (D == 64) {  // features 64-127 of Y: zeros that no load touches
@@ -609,16 +611,22 @@ __global__ void __launch_bounds__(1024, 1)
 }
 
 // The segments' own contributions (p.seg) into the state in front of each, in
-// the order of walking, and into the state behind the last.  Thread = 4 entries.
+// the order of walking, and into the state behind the last.  Thread = 4 entries;
+// eight segments' loads are in flight before the first is used (one at a time: 24
+// us for 12 segments of 12 heads).
 template <int D>
-__global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ DecayParams p) {
-    constexpr int PER = D * D / 4;
+__global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__ DecayParams p) {
+    constexpr int PER = D * D / 4, AHEAD = 8;
     const int bh = blockIdx.y, pi = blockIdx.z;
-    const int e4 = blockIdx.x * 256 + threadIdx.x;  // D * D / 4 is a multiple of 256
+    const int e4 = blockIdx.x * 128 + threadIdx.x;  // D * D / 4 is a multiple of 128
     const DecayPass& ps = p.pass[pi];
     const int len = decay_len(p.lens, bh / p.H, p.N);
     const double ld = decay_log(p.log_decay, bh % p.H);
     const size_t mat = static_cast<size_t>(bh) * PER;
+    float4* at = reinterpret_cast<float4*>(p.seg) + static_cast<size_t>(pi) * p.nseg * p.B * p.H * PER + mat + e4;
+    const size_t step = static_cast<size_t>(p.B) * p.H * PER;
+    const int whole = p.seg_chunks * kDecayChunk;  // tokens of a full segment
+    const double full = exp(ld * whole);
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (ps.init) {
         if (ps.transposed) {
@@ -629,19 +637,25 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__
             S = reinterpret_cast<const float4*>(ps.init)[mat + e4];
         }
     }
-    float4* at = reinterpret_cast<float4*>(p.seg) + static_cast<size_t>(pi) * p.nseg * p.B * p.H * PER + mat + e4;
-    const size_t step = static_cast<size_t>(p.B) * p.H * PER;
-    for (int i = 0; i < p.nseg; ++i) {
-        const int seg = ps.reverse ? p.nseg - 1 - i : i;
-        int c0, c1;
-        decay_span(len, seg, p.seg_chunks, &c0, &c1);
-        const int n = min(c1 * kDecayChunk, len) - min(c0 * kDecayChunk, len);
-        const double gd = exp(ld * n);
-        const float g = static_cast<float>(gd), g2 = static_cast<float>(gd - g);
-        const float4 own = at[seg * step];
-        at[seg * step] = S;
-        S.x = fmaf(g, S.x, fmaf(g2, S.x, own.x)), S.y = fmaf(g, S.y, fmaf(g2, S.y, own.y));
-        S.z = fmaf(g, S.z, fmaf(g2, S.z, own.z)), S.w = fmaf(g, S.w, fmaf(g2, S.w, own.w));
+    for (int i0 = 0; i0 < p.nseg; i0 += AHEAD) {
+        float4 own[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k, seg = ps.reverse ? p.nseg - 1 - i : i;
+            if (i < p.nseg) own[k] = at[seg * step];
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k, seg = ps.reverse ? p.nseg - 1 - i : i;
+            if (i >= p.nseg) break;
+            int n = len - seg * whole;
+            n = n < 0 ? 0 : (n > whole ? whole : n);
+            const double gd = n == whole ? full : exp(ld * n);
+            const float g = static_cast<float>(gd), g2 = static_cast<float>(gd - g);
+            at[seg * step] = S;
+            S.x = fmaf(g, S.x, fmaf(g2, S.x, own[k].x)), S.y = fmaf(g, S.y, fmaf(g2, S.y, own[k].y));
+            S.z = fmaf(g, S.z, fmaf(g2, S.z, own[k].z)), S.w = fmaf(g, S.w, fmaf(g2, S.w, own[k].w));
+        }
     }
     if (ps.last) reinterpret_cast<float4*>(ps.last)[mat + e4] = S;
 }
@@ -681,7 +695,7 @@ void decay_launch(const DecayMaps& maps, const DecayParams& p, cudaStream_t st) 
     const unsigned grid = static_cast<unsigned>(p.B) * p.H * (D / 64) * p.passes * p.nseg;
     if (p.nseg > 1) {
         decay_chunk_kernel<D, BF16, true><<<grid, 1024, bytes, st>>>(maps, p);
-        decay_scan_kernel<D><<<dim3(D * D / 1024, p.B * p.H, p.passes), 256, 0, st>>>(p);
+        decay_scan_kernel<D><<<dim3(D * D / 512, p.B * p.H, p.passes), 128, 0, st>>>(p);
     }
     decay_chunk_kernel<D, BF16, false><<<grid, 1024, bytes, st>>>(maps, p);
 }
