@@ -102,8 +102,8 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // 16 features); 4 hold the state (thread = feature of y); 8 make Zh (thread =
 // token, 32 features each).  Every role's work lies on the chain from one chunk to
 // the next (Zh is written when its last reader is done), so it is spread over as many
-// warps as the registers carry: with 8 + 4 + 4 warps the same work took XX us for the large-head
-// prompt.  Registers are dealt out
+// warps as the registers carry (8 + 4 + 4 warps: 103 us for the large-head
+// prompt where these take 87).  Registers are dealt out
 // between the warpgroups (setmaxnreg).  Issue order: A_0, then per chunk Y^T Zh, X S,
 // A of the next chunk, P Z: while the row warps read X S and hand over P, the
 // next A runs, and the next P is made during P Z and Y^T Zh.  Every product has a
@@ -122,11 +122,19 @@ struct DecayCfg {
     static constexpr uint32_t STAGE = XB + YB + ZB;
     static constexpr uint32_t OFF_ZH = 2 * STAGE;
     static constexpr uint32_t OFF_S = OFF_ZH + NP * ZB;  // D rows of 64 features
-    static constexpr uint32_t OFF_PW = OFF_S + D * 128u; // 32 zeros, L^0 .. L^128, L^31 .. L^0
+    // The result is staged for its TMA store in a buffer of its own or, where shared
+    // memory is full (bf16, D = 128), in its step's Z, whose reload then waits for
+    // the store (at D = 64 a buffer of its own takes a long prompt from 83 to 70 us;
+    // at D = 128 half of X's stage instead of Z's: forward 83.0 to 82.2, gradients
+    // 231 to 240 us).
+    static constexpr bool OWN_O = D == 64 || !BF16;
+    static constexpr uint32_t OFF_O = OWN_O ? OFF_S + D * 128u : XB + YB;
+    static constexpr uint32_t O_STEP = OWN_O ? 0u : STAGE;
+    static constexpr uint32_t OFF_PW = OFF_S + D * 128u + (OWN_O ? 16384u : 0u); // 32 zeros, L^0 .. L^128, L^31 .. L^0
     static constexpr uint32_t OFF_BAR = OFF_PW + (32 + 132 + 32) * 4;
     // two each of the loads and the products (by step parity), one of the rest
     static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_AF = 6, B_KVF = 8, B_QSD = 10, B_OD = 12,
-                         B_PF = 14, B_ZH = 15, B_KVE = 16, B_SSF = 17, B_OE = 18, B_DR = 19, B_ZE = 20,
+                         B_PF = 14, B_ZH = 15, B_KVE = 16, B_SSF = 17, B_OE = 18, B_DR = 19, B_OR = 20,
                          B_OW = 22, NBAR = 23;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -235,7 +243,9 @@ __global__ void __launch_bounds__(1024, 1)
                         tma_load_3d(sx + kb * 16384u, mx, DBAR(C::B_XF + s), kb * 64, row, bh);
                 }
                 issued = 3 * i + 2;
-                if (!STATE && i >= 2 && !(ok = wait_bounded(DBAR(C::B_ZE + s), par, abort_flag))) break;
+                if (!STATE && i >= 2 &&
+                    !(ok = wait_bounded(DBAR((C::OWN_O ? C::B_OD : C::B_OR) + s), par, abort_flag)))
+                    break;
                 mbar_arrive_expect_tx(DBAR(C::B_ZF + s), C::ZB);
                 tma_load_3d(sz, mz, DBAR(C::B_ZF + s), hf * 64, row, bh);
                 issued = 3 * i + 3;
@@ -324,18 +334,18 @@ __global__ void __launch_bounds__(1024, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ---------------------------------------------------------- output
-        // O_i, staged in the stage of Z_i, leaves by TMA; the stage is then free
+        // O_i leaves its staging by TMA
         if (!STATE && elect_one()) {
             for (int i = 0; i < nch; ++i) {
                 const int s = i & 1;
                 if (!wait_bounded(DBAR(C::B_OW), i & 1, abort_flag)) break;
                 if (tokens(i) == kDecayChunk) {
-                    tma_store_3d(&maps.m[ps.out_map], base + s * C::STAGE + C::XB + C::YB, hf * 64,
+                    tma_store_3d(&maps.m[ps.out_map], base + C::OFF_O + s * C::O_STEP, hf * 64,
                                  chunk(i) * kDecayChunk, bh);
                     bulk_commit();
                     bulk_wait_read_all();
                 }
-                mbar_arrive(DBAR(C::B_ZE + s));
+                mbar_arrive(DBAR(C::B_OR + s));
             }
             bulk_wait_all();
         }
@@ -426,12 +436,15 @@ __global__ void __launch_bounds__(1024, 1)
             for (int e = 0; e < 8; ++e)
                 o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
                                      fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
+            // the staging's previous content has left
+            if (C::OWN_O && i >= 1 &&
+                !__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OR + (b ^ 1)), ((i - 1) >> 1) & 1, abort_flag)))
+                break;
             if (n == kDecayChunk) {
-                // into the stage of Z, which P Z has read, as the TMA store expects it
-                // (16-byte piece j of row r at j ^ (r mod 8)).  Stored from registers, 32
-                // bytes of each row by a thread, every store was 32 wavefronts of L1: 31 of
-                // the large-head prompt's 103 us.
-                uint8_t* dst = gbase + b * C::STAGE + C::XB + C::YB + r * 128;
+                // as the TMA store expects it: 16-byte piece j of row r at j ^ (r mod 8).
+                // Stored from registers, 32 bytes of each row by a thread, every store was
+                // 32 wavefronts of L1: 31 of the large-head prompt's 103 us.
+                uint8_t* dst = gbase + C::OFF_O + b * C::O_STEP + r * 128;
                 *reinterpret_cast<uint4*>(dst + (((2 * cb) ^ (r & 7)) << 4)) = make_uint4(o16[0], o16[1], o16[2], o16[3]);
                 *reinterpret_cast<uint4*>(dst + (((2 * cb + 1) ^ (r & 7)) << 4)) =
                     make_uint4(o16[4], o16[5], o16[6], o16[7]);
