@@ -135,7 +135,7 @@ struct DecayCfg {
     // two each of the loads and the products (by step parity), one of the rest
     static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_AF = 6, B_KVF = 8, B_QSD = 10, B_OD = 12,
                          B_PF = 14, B_ZH = 15, B_KVE = 16, B_SSF = 17, B_OE = 18, B_DR = 19, B_OR = 20,
-                         B_OW = 22, NBAR = 23;
+                         B_OW = 22, NBAR = 24;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;
     static constexpr uint32_t COL_KV = 256, COL_O = 448;  // tensor memory: A at 0 and 128
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(1024, 1)
     const double ld = decay_log(p.log_decay, bh % p.H);
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
-            const int rows = i == C::B_PF || i == C::B_OE || i == C::B_OW;
+            const int rows = i == C::B_PF || i == C::B_OE || i >= C::B_OW;
             const int state = i == C::B_KVE || i == C::B_SSF;
             mbar_init(DBAR(i), rows ? C::NROW : (state ? C::NSTATE : (i == C::B_ZH ? C::NZH : 1)));
         }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(1024, 1)
         if (!STATE && elect_one()) {
             for (int i = 0; i < nch; ++i) {
                 const int s = i & 1;
-                if (!wait_bounded(DBAR(C::B_OW), i & 1, abort_flag)) break;
+                if (!wait_bounded(DBAR(C::B_OW + s), (i >> 1) & 1, abort_flag)) break;
                 if (tokens(i) == kDecayChunk) {
                     tma_store_3d(&maps.m[ps.out_map], base + C::OFF_O + s * C::O_STEP, hf * 64,
                                  chunk(i) * kDecayChunk, bh);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(1024, 1)
                 dst[0] = make_uint4(o16[0], o16[1], o16[2], o16[3]);
                 dst[1] = make_uint4(o16[4], o16[5], o16[6], o16[7]);
             }
-            mbar_arrive(DBAR(C::B_OW));
+            mbar_arrive(DBAR(C::B_OW + b));
         }
     } else if (warp < 24) {
         // -------------------------------------------------------- the state
