@@ -18,6 +18,7 @@
 #include "fp8_sm100.cuh"
 #include "linear_sm100.cuh"
 #include "cache8.cuh"
+#include "cache8_tile.cuh"
 #include "decay_sm100.cuh"
 
 namespace {
@@ -966,8 +967,8 @@ extern "C" int attn_cache_attend(const void* q, const unsigned char* k8, const u
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T;
     p.num_pages = num_pages, p.max_pages = max_pages;
     p.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
-    p.mtiles = attn::attend_mtiles(Hq, Hkv, T);
-    attn::attend_splits(B, Hkv, p.mtiles, max_len, &p.nsplit, &p.split);
+    p.mtiles = attn::attend_ctas(Hq, Hkv, T);
+    attn::attend_plan(B, Hq, Hkv, T, max_len, &p.nsplit, &p.split);
     if (1LL * p.mtiles * p.nsplit * Hkv * B >= (1LL << 31)) return ATTN_ERR_SHAPE;
     if (p.nsplit > 1 && !workspace) return ATTN_ERR_NULL;
     p.part = static_cast<float*>(workspace);

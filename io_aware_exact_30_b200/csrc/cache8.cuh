@@ -693,39 +693,4 @@ inline void attend_splits(int B, int Hkv, int mtiles, int max_len, int* nsplit, 
     *split = static_cast<int>(len);
 }
 
-inline size_t attend_workspace(int B, int Hq, int Hkv, int T, int D, int max_len) {
-    int nsplit, split;
-    attend_splits(B, Hkv, attend_mtiles(Hq, Hkv, T), max_len, &nsplit, &split);
-    return nsplit > 1 ? static_cast<size_t>(B) * Hq * T * nsplit * (D + 2) * 4 : 0;
-}
-
-template <int D, bool BF16>
-bool attend_set_attributes() {
-    return cudaFuncSetAttribute(cache_attend_kernel<D, BF16, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(AttendCfg<D, 1>::SMEM)) == cudaSuccess &&
-           cudaFuncSetAttribute(cache_attend_kernel<D, BF16, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(AttendCfg<D, 2>::SMEM)) == cudaSuccess;
-}
-
-template <int D, bool BF16>
-void attend_launch(const AttendParams& p, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>(p.mtiles) * p.nsplit * p.Hkv * p.B;
-    if (attend_rows(p.Hq, p.Hkv, p.T) == 8)
-        cache_attend_kernel<D, BF16, 1><<<grid, 128, AttendCfg<D, 1>::SMEM, st>>>(p);
-    else
-        cache_attend_kernel<D, BF16, 2><<<grid, 128, AttendCfg<D, 2>::SMEM, st>>>(p);
-    if (p.nsplit > 1) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hq * p.T);
-        cfg.blockDim = dim3(256);
-        cfg.stream = st;
-        cudaLaunchAttribute early;
-        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        early.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &early;
-        cfg.numAttrs = 1;
-        cudaLaunchKernelEx(&cfg, cache_attend_join_kernel<D, BF16>, p);
-    }
-}
-
 }  // namespace attn
