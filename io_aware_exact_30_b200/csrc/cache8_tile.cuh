@@ -1,23 +1,31 @@
 // Attention over the e4m3 cache for more than 16 query rows of a key/value head
 // (several tokens, or many query heads that share it): tensor-memory tiles.
 //
-// One CTA per (128 query rows, split, key/value head, sequence) walks its keys in
+// One CTA per (64 query rows, split, key/value head, sequence) walks its keys in
 // tiles of 128.  The codes are converted once for all rows:
 //   K -> fp16, exactly; the page's scale multiplies the scores in fp32
 //   V -> bf16, times the page's scale, exactly (4 significant bits, bf16 has fp32's
 //        range: no page is too far from another)
 //   Q -> fp16 by a power of two for each row, exact down to 2^-18 of its largest
-// S = Q K^T (tensor memory, two buffers), softmax with thread = row, P as two bf16
-// pieces (its rounding 2^-17), O += P_hi V + P_lo V (tensor memory).  The kept maximum
-// of a row moves when a score exceeds it by more than 2^6.
+// S = Q K^T and O += P V in tensor memory.  P goes to bf16 in two pieces (its rounding
+// 2^-17), and the two pieces are two rows of one product: lanes 64-127 repeat the
+// queries of lanes 0-63, make the same P and hand over its low piece, and O is the
+// sum of the two lanes.
 //
-// Bound by HBM for up to 128 rows: 32 KB of codes a tile take 1400 cycles of a
-// multiprocessor's share of bandwidth, the products about 1500 (S 512, P V twice 512),
-// the conversion about 620 issue slots of each scheduler.
+// bf16 has fp32's range, so P needs no running maximum to stay in bounds: a row's
+// reference is the maximum of the first tile in which it sees a key, and one pass
+// over S does a tile.  Only when a score exceeds the reference by more than 2^60 is the
+// reference moved, O rescaled and the tile's pass repeated.  Keys 0-63 and 64-127 of
+// the tiles are two softmaxes of their own, each with its reference, sum and output,
+// joined at the end: their warps never wait for one another.
 //
-// Roles (512 threads): warp 0 issues the products, warps 4-7 softmax and output,
-// warps 8-15 conversion: each 16 keys of a tile, which lie in one page; a lane
-// reads back, through shared memory, the 16-byte pieces it copied itself (cp.async).
+// Bound by XXX
+//
+// Roles (640 threads): warp 0 issues the products, warps 4-11 softmax (thread = lane;
+// four warps a half of the keys) and output, warps 12-19 conversion: each 16 keys of
+// a tile, which lie in one page; a lane reads back, through shared memory, the 16-byte
+// pieces it copied itself (cp.async).  P is packed over the columns of S that its
+// thread has read.
 #pragma once
 
 #include "cache8.cuh"
@@ -35,18 +43,20 @@ struct AttendTileCfg {
     // a tile's when the conversion is two tiles on
     static constexpr uint32_t OFF_KS = OFF_RAW + 8 * RAW_WARP;
     static constexpr uint32_t OFF_BAR = OFF_KS + 4 * 8 * 4;
-    static constexpr int B_KF = 0, B_VF = 2, B_SF = 4, B_SR = 6, B_OD = 8, B_PF = 10, B_QF = 11, B_DR = 12,
+    static constexpr int B_KF = 0, B_VF = 2, B_SF = 4, B_OD = 6, B_PF = 8, B_QF = 10, B_XF = 11, B_DR = 12,
                          NBAR = 13;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr uint32_t SMEM = OFF_MISC + 16 + 1024;
-    static constexpr uint32_t COL_P = 256, COL_O = 384;  // S at 0 and 128; P_hi, P_lo 64 columns each
+    static constexpr uint32_t COL_O = 256;  // S at 0 and 128, O of either half of the keys at 256 and 384
+    static_assert(8u * RAW_WARP >= 64u * 2 * 8, "room for the halves' statistics");
     static_assert(SMEM <= 232448u, "dynamic shared memory above the sm_100 per-block limit");
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendParams p) {
     using C = AttendTileCfg<D>;
-    constexpr float kRaise = 6.f;
+    constexpr float kRaise = 60.f;
+    constexpr int ROWS = 64;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw0 = smem_u32(smem_raw);
     const uint32_t base = (raw0 + 1023u) & ~1023u;
@@ -62,7 +72,7 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
     attend_lengths(p, b, &len, &tb, threadIdx.x == 0);
     const int G = p.Hq / p.Hkv, rows = G * tb;  // row r: query r / G of head hk G + r % G
     const int k0 = split * p.split;
-    if (mt * 128 >= rows || (split > 0 && k0 >= len)) return;
+    if (mt * ROWS >= rows || (split > 0 && k0 >= len)) return;
     const int k1 = split == p.nsplit - 1 ? len : min(len, k0 + p.split);
     const bool whole = p.nsplit == 1 || len <= p.split;
     const int nt = k1 > k0 ? (k1 - k0 + 127) >> 7 : 0;
@@ -72,7 +82,7 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
     volatile uint32_t* abort_flag = tmem_slot + 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(ABAR(i), i < C::B_SF ? 256 : ((i >= C::B_SR && i < C::B_OD) || i == C::B_PF || i == C::B_QF ? 128 : 1));
+            mbar_init(ABAR(i), i < C::B_SF || i == C::B_PF || i == C::B_PF + 1 || i == C::B_XF ? 256 : (i == C::B_QF ? 128 : 1));
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -94,10 +104,10 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
             const uint64_t dq = sdesc_sw128(base, 16, 1024), dk = sdesc_sw128(base + C::OFF_K, 16, 1024),
                            dv = sdesc_sw128(base + C::OFF_V, 16384, 1024);
             constexpr uint32_t M16 = C::MAT >> 4;
-            // S of tile j: its K written, S's buffer read by the softmax two tiles back
+            // S of tile j: its K written, its buffer (P of two tiles back) read by P V
             auto issue_s = [&](int j) -> bool {
                 const int s = j & 1;
-                if (!wait3(ABAR(C::B_KF + s), (j >> 1) & 1, true, ABAR(C::B_SR + s), ((j >> 1) - 1) & 1, j >= 2,
+                if (!wait3(ABAR(C::B_KF + s), (j >> 1) & 1, true, ABAR(C::B_OD + s), ((j >> 1) - 1) & 1, j >= 2,
                            ABAR(C::B_QF), 0, j == 0, abort_flag))
                     return false;
                 tc_fence_after();
@@ -113,16 +123,16 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
             for (int j = 0; ok && j < nt; ++j) {
                 const int s = j & 1;
                 if (j + 1 < nt && !(ok = issue_s(j + 1))) break;
-                if (!(ok = wait3(ABAR(C::B_PF), j & 1, true, ABAR(C::B_VF + s), (j >> 1) & 1, true, 0u, 0u, false,
+                if (!(ok = wait3(ABAR(C::B_PF + s), (j >> 1) & 1, true, ABAR(C::B_VF + s), (j >> 1) & 1, true, 0u, 0u, false,
                                  abort_flag)))
                     break;
                 tc_fence_after();
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)  // 16 keys (2048 bytes) per step
-                        mma_ts(tmem + C::COL_O, tmem + C::COL_P + 64u * h + kk * 8u, dv + s * M16 + kk * 128u, ID_O,
-                               (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk)  // 16 keys (2048 bytes) per step
+                        mma_ts(tmem + C::COL_O + 128u * h, tmem + 128u * s + 64u * h + kk * 8u,
+                               dv + s * M16 + (4 * h + kk) * 128u, ID_O, (j > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(ABAR(C::B_OD + s));
             }
             if (!ok) {
@@ -131,9 +141,9 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
             }
         }
         __syncwarp();
-    } else if (warp >= 8) {
+    } else if (warp >= 12) {
         // -------------------------------------------------------- conversion
-        const int w = warp - 8;
+        const int w = warp - 12;
         const int nw = k1 > k0 + 16 * w ? (k1 - k0 - 16 * w + 127) >> 7 : 0;  // tiles with keys of this warp
         // lane l looks up the page and scales of tile l of 32 at a time, one batch ahead
         auto look_up = [&](int batch, int& page, float& ks, float& vs) {
@@ -245,177 +255,207 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
         cp_async_wait<0>();
     } else if (warp >= 4) {
         // ------------------------------------------------ softmax and output
-        const int r = (warp & 3) * 32 + lane, rr = mt * 128 + r;  // row == TMEM lane
+        const int r = (warp & 3) * 32 + lane;       // TMEM lane
+        const int hf = (warp - 4) >> 2;             // keys 64 hf.. of the tiles
+        const bool low = (warp & 3) >= 2;           // the low pieces' lanes
+        const int rr = mt * ROWS + (r & 63);
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const bool mine = mt * 128 + (warp & 3) * 32 < rows;  // the warp has rows
+        const bool mine = mt * ROWS + (warp & 1) * 32 < rows;  // the warp has rows
         const size_t row = rr < rows
             ? (static_cast<size_t>(b) * p.Hq + hk * G + rr % G) * p.T + rr / G : 0;
-        float mul = 0.f;
-        int see = 0;
+        const int see = rr < rows ? min(k1, p.causal ? len - (tb - 1 - rr / G) : len) : 0;
+        float mul;
         {
             // the row into fp16 by a power of two, rows past the last zero
-            uint4 q[D / 8];
             uint32_t top = 0u;
+            const uint4* q = reinterpret_cast<const uint4*>(p.q + row * D * 2);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-                q[c] = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < rows) q[c] = __ldg(reinterpret_cast<const uint4*>(p.q + row * D * 2) + c);
-                top = __vmaxu2(__vmaxu2(top, q[c].x & 0x7fff7fffu), q[c].y & 0x7fff7fffu);
-                top = __vmaxu2(__vmaxu2(top, q[c].z & 0x7fff7fffu), q[c].w & 0x7fff7fffu);
+                const uint4 x = rr < rows ? __ldg(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+                top = __vmaxu2(__vmaxu2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
             }
             const float2 f = unpack2<BF16>(top);
             int e = 130 - static_cast<int>(__float_as_uint(fmaxf(f.x, f.y)) >> 23);
             e = e < -126 ? -126 : (e > 126 ? 126 : e);
             const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
             mul = p.scale_log2 / up;
-            if (rr < rows) see = p.causal ? len - (tb - 1 - rr / G) : len;
+            if (hf == 0) {
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint32_t x[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-                uint32_t h[4];
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = rr < rows ? __ldg(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t h[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 y = unpack2<BF16>(x[k]);
-                    h[k] = pack2<false>(y.x * up, y.y * up);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = unpack2<BF16>(x[k]);
+                        h[k] = pack2<false>(y.x * up, y.y * up);
+                    }
+                    *reinterpret_cast<uint4*>(gbase + (c >> 3) * 16384u + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
                 }
-                *reinterpret_cast<uint4*>(gbase + (c >> 3) * 16384u + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
+                fence_proxy_async_smem();
+                mbar_arrive(ABAR(C::B_QF));
             }
-            fence_proxy_async_smem();
-            mbar_arrive(ABAR(C::B_QF));
         }
-        if (see > k1) see = k1;
         const int all = __reduce_min_sync(0xffffffffu, rr < rows ? see : k1);  // keys all rows of the warp see
-        float m = -INFINITY, mb = 0.f, l = 0.f;
+        float m = -INFINITY, mb = 0.f, l = 0.f;  // reference, the same as a base (0 for none), sum
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            const int s = j & 1, key0 = k0 + j * 128;
+            const int s = j & 1, key0 = k0 + j * 128 + 64 * hf;
             if (!(ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_SF + s), (j >> 1) & 1, abort_flag)))) break;
             tc_fence_after();
-            float4 ks4[2] = {*reinterpret_cast<const float4*>(gbase + C::OFF_KS + (j & 3) * 32),
-                             *reinterpret_cast<const float4*>(gbase + C::OFF_KS + (j & 3) * 32 + 16)};
-            const float ks[8] = {ks4[0].x, ks4[0].y, ks4[0].z, ks4[0].w, ks4[1].x, ks4[1].y, ks4[1].z, ks4[1].w};
-            bool edge = key0 + 128 > all;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) edge |= ks[g] < 0.f;
-            // scores of 32 keys (two pages' worth of 16), log2 units
-            auto scores = [&](int cc, float (&x)[32]) {
-                uint32_t v[32];
-                tmem_ld32(lane_addr + 128u * s + 32u * cc, v);
-                tmem_ld_wait();
-                reg_fence32(v);
-                const float a = mul * ks[2 * cc], d = mul * ks[2 * cc + 1];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]) * (e < 16 ? a : d);
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (ks[2 * cc + (e >> 4)] < 0.f || key0 + 32 * cc + e >= see) x[e] = -INFINITY;
-                }
-            };
-            float top = -INFINITY;
+            const uint32_t cols = lane_addr + 128u * s + 64u * hf;
             if (mine) {
+                const float4 k4 = *reinterpret_cast<const float4*>(gbase + C::OFF_KS + (j & 3) * 32 + hf * 16);
+                const float ks[4] = {k4.x, k4.y, k4.z, k4.w};
+                const bool edge = key0 + 64 > all || k4.x < 0.f || k4.y < 0.f || k4.z < 0.f || k4.w < 0.f;
+                uint32_t v[4][16];  // S of the 64 keys
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) tmem_ld16(cols + 16u * cc, v[cc]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) reg_fence(v[cc][e]);
+                // exponents against the reference
+                float top = -INFINITY;
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
-                    float x[32];
-                    scores(cc, x);
+                    const float a = mul * ks[cc];
+                    const uint64_t a2 = f2(a, a), minus = f2(-mb, -mb);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) top = max3(top, x[e], x[e + 1]);
+                    for (int e = 0; e < 8; ++e) {
+                        float2 y = unf2(fma2(f2(__uint_as_float(v[cc][2 * e]), __uint_as_float(v[cc][2 * e + 1])), a2,
+                                             minus));
+                        if (edge) {
+                            const int key = key0 + 16 * cc + 2 * e;
+                            if (ks[cc] < 0.f || key >= see) y.x = -INFINITY;
+                            if (ks[cc] < 0.f || key + 1 >= see) y.y = -INFINITY;
+                        }
+                        top = max3(top, y.x, y.y);
+                        v[cc][2 * e] = __float_as_uint(y.x), v[cc][2 * e + 1] = __float_as_uint(y.y);
+                    }
                 }
-            }
-            // P's and O's last product is done: both may be written
-            if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_OD + (s ^ 1)), ((j - 1) >> 1) & 1, abort_flag))))
-                break;
-            tc_fence_after();
-            if (mine) {
-                if (__any_sync(0xffffffffu, top > m + kRaise)) {
-                    const float up = fmaxf(top, m);
-                    const float next = up == -INFINITY ? 0.f : up, keep = ex2(m - next);
-                    m = up, mb = next, l *= keep;
-                    if (j > 0) {
+                // the row's first keys, or a score far above the reference
+                const bool move = top > kRaise || (m == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xffffffffu, move)) {
+                    // (what a first reference scales is still zero)
+                    const float by = move ? top : 0.f, keep = m == -INFINITY ? 1.f : ex2(-by);
+                    mb += by;
+                    if (move) m = mb;
+                    l *= keep;
+                    if (j > 0) {  // O, once the last product is done
+                        if (!(ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_OD + (s ^ 1)), ((j - 1) >> 1) & 1,
+                                                                        abort_flag))))
+                            break;
+                        tc_fence_after();
 #pragma unroll
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            uint32_t v[32];
-                            tmem_ld32(lane_addr + C::COL_O + 32u * cc, v);
+                        for (int cc = 0; cc < D / 16; ++cc) {
+                            uint32_t x[16];
+                            tmem_ld16(lane_addr + C::COL_O + 128u * hf + 16u * cc, x);
                             tmem_ld_wait();
-                            reg_fence32(v);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
-                            tmem_st32(lane_addr + C::COL_O + 32u * cc, v);
+                            for (int e = 0; e < 16; ++e) {
+                                reg_fence(x[e]);
+                                x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
+                            }
+                            tmem_st16(lane_addr + C::COL_O + 128u * hf + 16u * cc, x);
                         }
                     }
-                }
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    float x[32];
-                    scores(cc, x);
-                    uint32_t hi[16], lo[16];
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[cc][e] = __float_as_uint(__uint_as_float(v[cc][e]) - by);
+                }
+                uint64_t sum = 0ull;
+#pragma unroll
+                for (int cc = 0; cc < 4; cc += 2) {
+                    uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float a = ex2(x[2 * e] - mb), d = ex2(x[2 * e + 1] - mb);
-                        l += a + d;
-                        hi[e] = pack2<true>(a, d);
-                        const float2 f = unpack2<true>(hi[e]);
-                        lo[e] = pack2<true>(a - f.x, d - f.y);
+                        const float pa = ex2(__uint_as_float(v[cc + (e >> 3)][2 * (e & 7)])),
+                                    pb = ex2(__uint_as_float(v[cc + (e >> 3)][2 * (e & 7) + 1]));
+                        sum = add2(sum, f2(pa, pb));
+                        pk[e] = pack2<true>(pa, pb);
+                        if (low) {
+                            const float2 f = unpack2<true>(pk[e]);
+                            pk[e] = pack2<true>(pa - f.x, pb - f.y);
+                        }
                     }
-                    tmem_st16(lane_addr + C::COL_P + 16u * cc, hi);
-                    tmem_st16(lane_addr + C::COL_P + 64u + 16u * cc, lo);
+                    tmem_st16(cols + 8u * cc, pk);
                 }
+                const float2 f = unf2(sum);
+                l += f.x + f.y;
                 tmem_st_wait();
-            } else if (j == 0) {  // rows past the last: P stays zero
+            } else {  // lanes of rows past the last: P = 0
                 uint32_t none[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) none[e] = 0u;
-#pragma unroll
-                for (int cc = 0; cc < 8; ++cc) tmem_st16(lane_addr + C::COL_P + 16u * cc, none);
+                tmem_st16(cols, none);
+                tmem_st16(cols + 16u, none);
                 tmem_st_wait();
             }
             tc_fence_before();
-            mbar_arrive(ABAR(C::B_SR + s));
-            mbar_arrive(ABAR(C::B_PF));
+            mbar_arrive(ABAR(C::B_PF + s));
         }
         if (ok && nt > 0)
             ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_OD + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, abort_flag));
         tc_fence_after();
-        if (ok && mine) {
-            const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        // join: the four parts of a row (half of the keys, piece of P) through the
+        // memory of K and V, which the products have read
+        float* parts = reinterpret_cast<float*>(gbase + C::OFF_K);        // (part, feature, row)
+        float2* ml = reinterpret_cast<float2*>(gbase + C::OFF_RAW);       // (half, row)
+        if (ok) {
+            float* x = parts + (hf * 2 + (low ? 1 : 0)) * D * 64 + (r & 63);
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t v[32];
+            for (int cc = 0; cc < D / 16; ++cc) {
+                uint32_t v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = 0u;
                 if (nt > 0) {
-                    tmem_ld32(lane_addr + C::COL_O + 32u * cc, v);
+                    tmem_ld16(lane_addr + C::COL_O + 128u * hf + 16u * cc, v);
                     tmem_ld_wait();
-                    reg_fence32(v);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
-                if (rr < rows) {
-                    if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.o + (row * D + 32 * cc) * 2);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t h[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                h[k] = pack2<BF16>(__uint_as_float(v[8 * e + 2 * k]) * inv,
-                                                   __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-                            dst[e] = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part + (row * p.nsplit + split) * D + 32 * cc);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                                 __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                    }
+                for (int e = 0; e < 16; ++e) {
+                    reg_fence(v[e]);
+                    x[(16 * cc + e) * 64] = __uint_as_float(v[e]);
                 }
             }
-            if (rr < rows) {
+            if (!low) ml[hf * 64 + (r & 63)] = make_float2(m, l);
+            mbar_arrive(ABAR(C::B_XF));
+            ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_XF), 0, abort_flag));
+        }
+        const int t = threadIdx.x - 128, q = t & 63, part = t >> 6, qq = mt * ROWS + q;
+        if (ok && qq < rows) {
+            const float2 a = ml[q], d = ml[64 + q];
+            const float mm = fmaxf(a.x, d.x);
+            const float fa = a.x == -INFINITY ? 0.f : ex2(a.x - mm), fd = d.x == -INFINITY ? 0.f : ex2(d.x - mm);
+            const float ll = fa * a.y + fd * d.y;
+            const float inv = whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f;
+            const size_t at = (static_cast<size_t>(b) * p.Hq + hk * G + qq % G) * p.T + qq / G;
+#pragma unroll 4
+            for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 4) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float* x = parts + (c + e) * 64 + q;
+                    // (a half whose row saw nothing holds zeros)
+                    v[e] = (fa * (x[0] + x[D * 64]) + fd * (x[2 * D * 64] + x[3 * D * 64])) * inv;
+                }
                 if (whole)
-                    p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                    *reinterpret_cast<uint2*>(p.o + (at * D + c) * 2) =
+                        make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
                 else
-                    p.part_ml[row * p.nsplit + split] = make_float2(m, l);
+                    *reinterpret_cast<float4*>(p.part + (at * p.nsplit + split) * D + c) =
+                        make_float4(v[0], v[1], v[2], v[3]);
+            }
+            if (part == 0) {
+                if (whole)
+                    p.lse[at] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                else
+                    p.part_ml[at * p.nsplit + split] = make_float2(mm, ll);
             }
         }
     }
@@ -433,7 +473,9 @@ __global__ void __launch_bounds__(512, 1) cache_attend_tile_kernel(const AttendP
 // for more.
 inline bool attend_tiled(int Hq, int Hkv, int T) { return Hq / Hkv * T > 16; }
 inline int attend_ctas(int Hq, int Hkv, int T) {
-    return attend_tiled(Hq, Hkv, T) ? (Hq / Hkv * T + 127) / 128 : attend_mtiles(Hq, Hkv, T);
+    const int rows = Hq / Hkv * T;
+    if (!attend_tiled(Hq, Hkv, T)) return attend_mtiles(Hq, Hkv, T);
+    return (rows + 63) / 64;
 }
 inline void attend_plan(int B, int Hq, int Hkv, int T, int max_len, int* nsplit, int* split) {
     const int mtiles = attend_ctas(Hq, Hkv, T);
@@ -468,7 +510,7 @@ template <int D, bool BF16>
 void attend_launch(const AttendParams& p, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(p.mtiles) * p.nsplit * p.Hkv * p.B;
     if (attend_tiled(p.Hq, p.Hkv, p.T))
-        cache_attend_tile_kernel<D, BF16><<<grid, 512, AttendTileCfg<D>::SMEM, st>>>(p);
+        cache_attend_tile_kernel<D, BF16><<<grid, 640, AttendTileCfg<D>::SMEM, st>>>(p);
     else if (attend_rows(p.Hq, p.Hkv, p.T) == 8)
         cache_attend_kernel<D, BF16, 1><<<grid, 128, AttendCfg<D, 1>::SMEM, st>>>(p);
     else
