@@ -94,6 +94,16 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // registers of a thread by role; the launch gives each of the five warpgroups 96
+    constexpr int R_ISSUE = 32, R_SOFT = 136, R_CONV = 80;
+    static_assert(R_ISSUE + 2 * R_SOFT + 2 * R_CONV <= 5 * 96, "more registers than the launch has");
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R_ISSUE));
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R_SOFT));
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R_CONV));
+    }
     if (warp == 0) {
         // ------------------------------------------------------- MMA issuer
         uint32_t elected;
@@ -374,13 +384,18 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float pa = ex2(__uint_as_float(v[cc + (e >> 3)][2 * (e & 7)])),
-                                    pb = ex2(__uint_as_float(v[cc + (e >> 3)][2 * (e & 7) + 1]));
+                        uint32_t &a = v[cc + (e >> 3)][2 * (e & 7)], &d = v[cc + (e >> 3)][2 * (e & 7) + 1];
+                        const float pa = ex2(__uint_as_float(a)), pb = ex2(__uint_as_float(d));
                         sum = add2(sum, f2(pa, pb));
                         pk[e] = pack2<true>(pa, pb);
-                        if (low) {
+                        a = __float_as_uint(pa), d = __float_as_uint(pb);
+                    }
+                    if (low) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
                             const float2 f = unpack2<true>(pk[e]);
-                            pk[e] = pack2<true>(pa - f.x, pb - f.y);
+                            pk[e] = pack2<true>(__uint_as_float(v[cc + (e >> 3)][2 * (e & 7)]) - f.x,
+                                                __uint_as_float(v[cc + (e >> 3)][2 * (e & 7) + 1]) - f.y);
                         }
                     }
                     tmem_st16(cols + 8u * cc, pk);
