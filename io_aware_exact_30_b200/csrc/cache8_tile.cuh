@@ -329,24 +329,37 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
 #pragma unroll
                     for (int e = 0; e < 16; ++e) reg_fence(v[cc][e]);
                 // exponents against the reference
-                float top = -INFINITY;
+                const uint64_t minus = f2(-mb, -mb);
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
                     const float a = mul * ks[cc];
-                    const uint64_t a2 = f2(a, a), minus = f2(-mb, -mb);
+                    const uint64_t a2 = f2(a, a);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        float2 y = unf2(fma2(f2(__uint_as_float(v[cc][2 * e]), __uint_as_float(v[cc][2 * e + 1])), a2,
-                                             minus));
-                        if (edge) {
-                            const int key = key0 + 16 * cc + 2 * e;
-                            if (ks[cc] < 0.f || key >= see) y.x = -INFINITY;
-                            if (ks[cc] < 0.f || key + 1 >= see) y.y = -INFINITY;
-                        }
-                        top = max3(top, y.x, y.y);
+                        const float2 y = unf2(fma2(f2(__uint_as_float(v[cc][2 * e]), __uint_as_float(v[cc][2 * e + 1])),
+                                                   a2, minus));
                         v[cc][2 * e] = __float_as_uint(y.x), v[cc][2 * e + 1] = __float_as_uint(y.y);
                     }
                 }
+                if (edge) {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) {
+                        const int last = ks[cc] < 0.f ? 0 : see - (key0 + 16 * cc);  // keys seen of the 16
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (e >= last) v[cc][e] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float tops[4];
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    tops[cc] = __uint_as_float(v[cc][0]);
+#pragma unroll
+                    for (int e = 1; e < 15; e += 2)
+                        tops[cc] = max3(tops[cc], __uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1]));
+                    tops[cc] = fmaxf(tops[cc], __uint_as_float(v[cc][15]));
+                }
+                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
                 // the row's first keys, or a score far above the reference
                 const bool move = top > kRaise || (m == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, move)) {
