@@ -331,10 +331,13 @@ int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned cha
  * attn_decay_step: the recurrent form for one token, N = 1; state_out may be
  * state_in.
  *
- * workspace: attn_decay_workspace_bytes() bytes, 16-byte aligned (NULL when that
- * is 0); its contents on entry do not matter.  States are fp32 throughout;
- * chunked products with a state or with in-chunk weights see them rounded to
- * the input's 16-bit type.  Errors as attn_fwd.
+ * Results must not share memory with inputs (ATTN_ERR_ARG where an o, dq, dk or
+ * dv is one of the arrays read, or another result).  workspace:
+ * attn_decay_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0); its
+ * contents on entry do not matter.  Every sum is made in a fixed order: results
+ * repeat bit for bit.  States are fp32 throughout (errors of about 2^-22); in the
+ * chunked forms the 16-bit results see a state and the in-chunk weights rounded to
+ * their type.  Errors as attn_fwd.
  */
 size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward);
 

@@ -1043,6 +1043,8 @@ extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const
     const void* opt[] = {state_in, state_out, workspace};
     if (!log_decay) return ATTN_ERR_NULL;
     if (!aligned4(log_decay) || !aligned4(lens)) return ATTN_ERR_ALIGN;
+    // a head's CTAs read what others' results would overwrite
+    if (o && (o == q || o == k || o == v)) return ATTN_ERR_ARG;
     int dev;
     int rc = check_decay(req, 4, opt, 3, B, H, N, d, dtype, scale, &dev);
     if (rc) return rc;
@@ -1064,6 +1066,9 @@ extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const
     if (!log_decay) return ATTN_ERR_NULL;
     if (!aligned4(log_decay) || !aligned4(lens)) return ATTN_ERR_ALIGN;
     if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in)) return ATTN_ERR_ARG;
+    for (int i = 4; i < 7; ++i)
+        for (int j = 0; j < i; ++j)
+            if (req[i] && req[i] == req[j]) return ATTN_ERR_ARG;
     int dev;
     int rc = check_decay(req, 7, opt, 4, B, H, N, d, dtype, scale, &dev);
     if (rc) return rc;
@@ -1084,6 +1089,7 @@ extern "C" int attn_decay_step(const void* q, const void* k, const void* v, cons
     const void* req[] = {q, k, v, state_in, o, state_out};
     if (!log_decay) return ATTN_ERR_NULL;
     if (!aligned4(log_decay)) return ATTN_ERR_ALIGN;
+    if (o && (o == q || o == k || o == v)) return ATTN_ERR_ARG;
     int dev;
     int rc = check_decay(req, 6, nullptr, 0, B, H, 1, d, dtype, scale, &dev);
     if (rc) return rc;

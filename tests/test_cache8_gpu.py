@@ -208,6 +208,52 @@ def test_attend_scales_far_apart_and_masked_garbage():
     check_attend(q, cache, table, lens)
 
 
+@pytest.mark.parametrize("d,dtype,Hq,T", [(128, "bf16", 12, 3), (64, "bf16", 40, 2), (128, "fp16", 6, 13)])
+def test_attend_many_rows(d, dtype, Hq, T):
+    """More than 16 rows of a key/value head (tensor-memory tiles): long sequences in
+    several splits, sequences shorter than their queries, pages that end inside a
+    tile, scales 2^60 apart, zero and bad pages, garbage past the last token."""
+    lens = [1500, T - 1, 129, 0, 3000, 640]
+    page, B = 16, len(lens)
+    P, table = tables(B, 190, 40)
+    cache = filled_cache(P, 1, page, d, 41)
+    t = table.cpu().long()
+    if dtype == "bf16":
+        cache.v_scale[t[0, 3]] = 2.0 ** -40
+        cache.v_scale[t[0, 60]] = 2.0 ** 20
+    cache.v_scale[t[4, :9]] = 0.0
+    cache.k_scale[t[4, 20:40]] = 0.0
+    for c in (cache.k.view(torch.uint8), cache.v.view(torch.uint8)):
+        c[t[2, 8], :, lens[2] - 128:] = 0x7F
+        c[t[5, 40:]] = 0xFF
+    q = torch.randn(B, Hq, T, d, generator=torch.Generator().manual_seed(42)).to(TYPES[dtype]).cuda()
+    for causal in (True, False):
+        check_attend(q, cache, table, lens, causal)
+        check_attend(q, cache, table, lens, causal, q_lens=[T, 1, 0, T, 2, T - 1], max_len=700)
+    table[4, 100], table[0, 0] = -7, P
+    check_attend(q, cache, table, lens, bad=True)
+
+
+def test_attend_scores_that_climb_past_every_reference():
+    """Keys whose scores grow by hundreds of log2 units from tile to tile, first far
+    below, then far above where a row began: the weight ends on the last ones."""
+    for Hq in (4, 20):
+        page, d, n = 64, 128, 640
+        P, table = tables(1, n // page, 43)
+        cache = filled_cache(P, 1, page, d, 44)
+        order = table.cpu().long()[0]
+        for i, pg in enumerate(order):
+            cache.k_scale[pg] = 2.0 ** (-6 + i)
+        q = torch.randn(1, Hq, 1, d, generator=torch.Generator().manual_seed(45)).bfloat16().cuda()
+        check_attend(q, cache, table, [n])
+        for i, pg in enumerate(order):
+            cache.k_scale[pg] = 2.0 ** (3 - i)
+        check_attend(q, cache, table, [n])
+        cache.k.copy_(cache.k.float().abs().to(torch.float8_e4m3fn))
+        for sign in (-1, 1):
+            check_attend(sign * q.abs(), cache, table, [n - 13])
+
+
 def test_attend_bad_pages_are_not_seen():
     page, d = 32, 64
     P, table = tables(4, 4, 17)

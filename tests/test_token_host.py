@@ -24,17 +24,21 @@ def attend(p=P, B=2, Hq=4, Hkv=2, T=3, d=64, num_pages=8, page=16, width=4, max_
                                         num_pages, page, width, max_len, 1, scale, dt, None)
 
 
-def fwd(p=P, B=2, H=2, N=5, d=64, scale=0.1, dt=0, q=None, ld=P, st=P):
-    return attn.lib().attn_decay_fwd(q or p, p, p, ld, st, None, p, st, p, B, H, N, d, scale, dt, None)
+def at(i):
+    return ctypes.c_void_p(4096 * i)
 
 
-def bwd(p=P, B=2, H=2, N=5, d=64, scale=0.1, dt=0, q=None, ld=P, ds=ctypes.c_void_p(512)):
-    return attn.lib().attn_decay_bwd(q or p, p, p, ld, p, p, p, None, p, p, p, ds, p, B, H, N, d, scale, dt,
-                                     None)
+def fwd(p=P, B=2, H=2, N=5, d=64, scale=0.1, dt=0, q=None, ld=P, st=P, o=at(1)):
+    return attn.lib().attn_decay_fwd(q or p, p, p, ld, st, None, p and o, st, p, B, H, N, d, scale, dt, None)
 
 
-def step(p=P, B=2, H=2, d=64, scale=0.1, dt=0, q=None, ld=P):
-    return attn.lib().attn_decay_step(q or p, p, p, ld, p, p, p, B, H, d, scale, dt, None)
+def bwd(p=P, B=2, H=2, N=5, d=64, scale=0.1, dt=0, q=None, ld=P, ds=ctypes.c_void_p(512), g=(at(1), at(2), at(3))):
+    return attn.lib().attn_decay_bwd(q or p, p, p, ld, p, p, p, None, *(p and x for x in g), ds, p, B, H, N, d,
+                                     scale, dt, None)
+
+
+def step(p=P, B=2, H=2, d=64, scale=0.1, dt=0, q=None, ld=P, o=at(1)):
+    return attn.lib().attn_decay_step(q or p, p, p, ld, p, p and o, p, B, H, d, scale, dt, None)
 
 
 ALL = (append, attend, fwd, bwd, step)
@@ -72,6 +76,8 @@ def test_decay_refusals():
         assert call(H=0) == -2
     assert fwd(N=0) == -2 and bwd(N=0) == -2
     assert bwd(ds=P) == -9  # the gradient over an array that is read
+    assert fwd(o=P) == -9 and step(o=P) == -9  # a result over an input
+    assert bwd(g=(P, at(2), at(3))) == -9 and bwd(g=(at(1), at(2), at(1))) == -9
     assert attn.strerror(-11) and attn.strerror(-11) != attn.strerror(-99)
 
 
