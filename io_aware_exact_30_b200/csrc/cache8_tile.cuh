@@ -29,6 +29,7 @@
 #pragma once
 
 #include "cache8.cuh"
+#include "ptx_more.cuh"
 
 namespace attn {
 
@@ -98,17 +99,15 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
     constexpr int R_ISSUE = 32, R_SOFT = 136, R_CONV = 80;
     static_assert(R_ISSUE + 2 * R_SOFT + 2 * R_CONV <= 5 * 96, "more registers than the launch has");
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R_ISSUE));
+        regs_down<R_ISSUE>();
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R_SOFT));
+        regs_up<R_SOFT>();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R_CONV));
+        regs_down<R_CONV>();
     }
     if (warp == 0) {
         // ------------------------------------------------------- MMA issuer
-        uint32_t elected;
-        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
-        if (elected) {
+        if (elect_one()) {
             constexpr uint32_t ID_S = idesc_f16(false, 128, 128, false, false);  // Q K^T, fp16
             constexpr uint32_t ID_O = idesc_f16(true, 128, D, false, true);      // P V, bf16
             const uint64_t dq = sdesc_sw128(base, 16, 1024), dk = sdesc_sw128(base + C::OFF_K, 16, 1024),

@@ -14,7 +14,7 @@
 // decay.
 #pragma once
 
-#include "ptx.cuh"
+#include "ptx_more.cuh"
 
 namespace attn {
 
@@ -38,16 +38,6 @@ struct DecayParams {
     int nseg, seg_chunks;    // a sequence's chunks in segments of seg_chunks
     float scale;
 };
-
-// One lane of a converged warp.  A branch on it, unlike one on a lane index, tells
-// the compiler that a single thread runs what follows: the products' operands
-// then stay in uniform registers (8 products of N = 64 with A in tensor memory:
-// 265 cycles, against 431 behind lane == 0).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
 
 struct DecayMaps {
     CUtensorMap m[7];
@@ -145,15 +135,6 @@ struct DecayCfg {
     static_assert(R_ISSUE + 4 * R_ROW + R_STATE + 2 * R_ZH <= 8 * 64, "more registers than the launch has");
     static_assert(SMEM_BYTES <= 232448u, "dynamic shared memory above the sm_100 per-block limit");
 };
-
-template <int N>
-__device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 template <int D, bool BF16, bool STATE>
 __global__ void __launch_bounds__(1024, 1)
