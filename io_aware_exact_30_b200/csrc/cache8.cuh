@@ -268,12 +268,14 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) cache_attend_kernel(cons
     const int G = p.Hq / p.Hkv, rows = G * tb;  // row r: query r / G of head hk G + r % G
     const int k0 = split * p.split;
     if (mt * ROWS >= rows || (split > 0 && k0 >= len)) return;
-    const int k1 = split == p.nsplit - 1 ? len : min(len, k0 + p.split);
+    // keys past the last row's own position are seen by none of these rows
+    const int seen = p.causal ? len - (tb - 1 - (min(rows, (mt + 1) * ROWS) - 1) / G) : len;
+    const int k1 = min(seen, split == p.nsplit - 1 ? len : min(len, k0 + p.split));
     const bool whole = p.nsplit == 1 || len <= p.split;
     // --------------------------------------------- this warp's 16-key tiles
     // Step s is tile 4 s + warp; lane l looks up the page and scales of step l of 32
     // at a time, one batch ahead.
-    const int tile0 = k0 >> 4, ntiles = (k1 - k0 + 15) >> 4;  // splits start at tiles
+    const int tile0 = k0 >> 4, ntiles = k1 > k0 ? (k1 - k0 + 15) >> 4 : 0;  // splits start at tiles
     const int nsteps = (ntiles + 3 - warp) >> 2;              // of this warp
     auto look_up = [&](int batch, int& page, float& ks, float& vs) {
         const int step = batch * 32 + lane, tile = tile0 + 4 * step + warp;

@@ -74,7 +74,9 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
     const int G = p.Hq / p.Hkv, rows = G * tb;  // row r: query r / G of head hk G + r % G
     const int k0 = split * p.split;
     if (mt * ROWS >= rows || (split > 0 && k0 >= len)) return;
-    const int k1 = split == p.nsplit - 1 ? len : min(len, k0 + p.split);
+    // keys past the last row's own position are seen by none of these rows
+    const int seen = p.causal ? len - (tb - 1 - (min(rows, (mt + 1) * ROWS) - 1) / G) : len;
+    const int k1 = min(seen, split == p.nsplit - 1 ? len : min(len, k0 + p.split));
     const bool whole = p.nsplit == 1 || len <= p.split;
     const int nt = k1 > k0 ? (k1 - k0 + 127) >> 7 : 0;
     const uint32_t bar0 = base + C::OFF_BAR;
@@ -507,9 +509,13 @@ inline int attend_ctas(int Hq, int Hkv, int T) {
 inline void attend_plan(int B, int Hq, int Hkv, int T, int max_len, int* nsplit, int* split) {
     const int mtiles = attend_ctas(Hq, Hkv, T);
     if (!attend_tiled(Hq, Hkv, T)) return attend_splits(B, Hkv, mtiles, max_len, nsplit, split);
-    // two rounds of one CTA a multiprocessor, splits of four tiles at least
+    // One CTA a multiprocessor.  One round of them where two splits or more fit into
+    // it, else three (uneven lengths even out); splits of four tiles at least.
     if (max_len > (1 << 30)) max_len = 1 << 30;
-    long long len = 1LL * B * Hkv * mtiles * max_len / (148 * 2);
+    const long long base = 1LL * B * Hkv * mtiles;
+    long long n = 148 / base;
+    if (n < 2) n = (3 * 148 + base - 1) / base;
+    long long len = (max_len + n - 1) / n;
     len = (len + 127) / 128 * 128;
     if (len < 512) len = 512;
     if (len > (1 << 30)) len = 1 << 30;
