@@ -967,8 +967,8 @@ extern "C" int attn_cache_attend(const void* q, const unsigned char* k8, const u
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T;
     p.num_pages = num_pages, p.max_pages = max_pages;
     p.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
-    p.mtiles = attn::attend_ctas(Hq, Hkv, T);
-    attn::attend_plan(B, Hq, Hkv, T, max_len, &p.nsplit, &p.split);
+    const attn::AttendPlan plan = attn::attend_plan(B, Hq, Hkv, T, max_len);
+    p.mtiles = plan.mtiles, p.nsplit = plan.nsplit, p.split = plan.split;
     if (1LL * p.mtiles * p.nsplit * Hkv * B >= (1LL << 31)) return ATTN_ERR_SHAPE;
     if (p.nsplit > 1 && !workspace) return ATTN_ERR_NULL;
     p.part = static_cast<float*>(workspace);
@@ -978,9 +978,9 @@ extern "C" int attn_cache_attend(const void* q, const unsigned char* k8, const u
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool bf = dtype == ATTN_BF16;
     if (d == 64)
-        bf ? attn::attend_launch<64, true>(p, st) : attn::attend_launch<64, false>(p, st);
+        bf ? attn::attend_launch<64, true>(plan, p, st) : attn::attend_launch<64, false>(plan, p, st);
     else
-        bf ? attn::attend_launch<128, true>(p, st) : attn::attend_launch<128, false>(p, st);
+        bf ? attn::attend_launch<128, true>(plan, p, st) : attn::attend_launch<128, false>(plan, p, st);
     return launch_ok() ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 

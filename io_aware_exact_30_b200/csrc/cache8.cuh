@@ -51,8 +51,9 @@ struct AppendParams {
 // registers (16 bytes a thread and step), while their largest magnitude is
 // found; it decides the scale, and the rows are stored as codes.
 //
-// Bound by HBM for prompts (2 bytes read, 1 written per value) and by the
-// launch for single tokens.
+// Bound by HBM for prompts (2 bytes read, 1 written per value: four of up to 4096
+// tokens, 16 heads, d = 128: 26 us, 5.5 TB/s) and by the launch and two dependent
+// loads for single tokens (64 sequences, 8 heads: 4.5 us).
 template <int D, bool BF16, int NCH>
 __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p) {
     constexpr int PER_ROW = D / 8;  // 16-byte pieces of a row
@@ -238,6 +239,14 @@ __device__ __forceinline__ void attend_lengths(const AttendParams& p, int b, int
 // 64, and of V rows 2t, 2t+1, 2t+8, 2t+9 the features D/8 g .., a byte permute
 // pairing two keys' codes.  Each lane thus reads, through shared memory, only what
 // it copied itself (cp.async): no barrier but its own copies'.
+//
+// What bounds it: with 8 rows HBM and instruction latency at 16 warps an SM (128
+// registers): 64 sequences of 2.7 to 8 thousand tokens, 8 key/value heads, d = 128:
+// 155 us, 4.6 TB/s (5 CTAs an SM at 96 registers: 184; 3 at 150: 159; the query rows in
+// the wide extent of the fragments, 16 of which a single token fills one: 239).  Few
+// heads: the launch, four dependent loads and the join: 16 heads of 4096 tokens 12.5 us.
+// 16 rows convert the codes once for two fragments: 60 us for 16 x 2 heads of 16000
+// tokens where 8 rows take 37.
 template <int D, int NT>
 struct AttendCfg {
     static constexpr int KP = D / 32, VP = 4;  // pieces of 16 keys: K 16 bytes each, V D/8 bytes
@@ -670,19 +679,16 @@ __global__ void __launch_bounds__(256) cache_attend_join_kernel(const AttendPara
 }
 
 // Rows of a CTA: 8, or 16 when there are more than 8 (the codes' conversion is
-// then shared by two fragments of rows).
-inline int attend_rows(int Hq, int Hkv, int T) { return Hq / Hkv * T > 8 ? 16 : 8; }
-inline int attend_mtiles(int Hq, int Hkv, int T) {
-    const int rows = attend_rows(Hq, Hkv, T);
-    return (Hq / Hkv * T + rows - 1) / rows;
-}
+// then shared by two fragments of rows; with 24 or 40 rows a CTA, for 40 rows in
+// all, 102 and 98 us against 94: fewer conversions, but fewer warps).
+inline int attend_rows(int rows) { return rows > 8 ? 16 : 8; }
 
 // Splits of a call whose sequences hold at most max_len tokens: four rounds of
-// CTAs on the device's 148 multiprocessors (uneven lengths even out), but not
+// CTAs on the device's 148 multiprocessors (uneven lengths even out; the batch of 64
+// takes 179, 174, 160, 155 and 155 us with one, two, three, four and six), but not
 // below kLong tokens a split, then one round, but not below 256.
 inline void attend_splits(int B, int Hkv, int mtiles, int max_len, int* nsplit, int* split) {
     constexpr long long kRound = 148 * 4, kLong = 1024, kShort = 256;
-    if (max_len > (1 << 30)) max_len = 1 << 30;  // split * nsplit stays an int
     const long long tokens = 1LL * B * Hkv * mtiles * max_len;
     long long len = tokens / (kRound * 4);
     if (len < kLong) {

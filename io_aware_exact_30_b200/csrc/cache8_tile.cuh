@@ -19,7 +19,13 @@
 // the tiles are two softmaxes of their own, each with its reference, sum and output,
 // joined at the end: their warps never wait for one another.
 //
-// Bound by XXX
+// What bounds it: the softmax warps' chain (64 keys of a row a thread: about 2000
+// cycles a tile, its exponentials alone 1000), where the products take 1024 and a
+// tile's 32 KB of codes 1400 of a multiprocessor's share of HBM; and 8 us before a CTA's
+// first tile and after its last.  Measured: five queries of 8 heads a key/value head
+// over 16 sequences of 5 to 16 thousand tokens, d = 128: 64 us (16-row fragments, which
+// convert the codes three times: 94); 64 rows over 16000 tokens each: 68 us; 8192
+// queries of 32 heads over themselves (8 key/value heads): 1.72 ms, 320 TFLOP/s.
 //
 // Roles (640 threads): warp 0 issues the products, warps 4-11 softmax (thread = lane;
 // four warps a half of the keys) and output, warps 12-19 conversion: each 16 keys of
@@ -498,35 +504,46 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
     }
 }
 
-// Which form a call takes: fragments for up to 16 rows of a key/value head, tiles
-// for more.
-inline bool attend_tiled(int Hq, int Hkv, int T) { return Hq / Hkv * T > 16; }
-inline int attend_ctas(int Hq, int Hkv, int T) {
+// How a call runs: tensor-memory tiles of 64 rows of a key/value head, or fragments
+// of 8 or 16 rows a CTA; CTAs for its rows; splits.
+struct AttendPlan {
+    bool tiled;
+    int rows, mtiles, nsplit, split;
+};
+
+// Tiles for more than 16 rows, of which a tile costs one as much as another: 24 rows
+// over 16 x 2 heads of 16000 tokens take 62 us in tiles and 91 in fragments at d = 128
+// (53 and 58 at d = 64), 16 rows 60 and 59 (52 and 37).  Up to 32 rows over few keys
+// the fragments' shorter start counts: 32 rows over 8 heads of 4000 tokens 15.5 us
+// against 17.3, over 4 x 2 heads of 500 tokens 12.6 against 15.1.
+inline AttendPlan attend_plan(int B, int Hq, int Hkv, int T, int max_len) {
+    AttendPlan p;
+    if (max_len > (1 << 30)) max_len = 1 << 30;  // split * nsplit stays an int
     const int rows = Hq / Hkv * T;
-    if (!attend_tiled(Hq, Hkv, T)) return attend_mtiles(Hq, Hkv, T);
-    return (rows + 63) / 64;
-}
-inline void attend_plan(int B, int Hq, int Hkv, int T, int max_len, int* nsplit, int* split) {
-    const int mtiles = attend_ctas(Hq, Hkv, T);
-    if (!attend_tiled(Hq, Hkv, T)) return attend_splits(B, Hkv, mtiles, max_len, nsplit, split);
+    p.tiled = rows > 32 || (rows > 16 && 1LL * B * Hkv * max_len > (1 << 17));
+    p.rows = p.tiled ? 64 : attend_rows(rows);
+    p.mtiles = (rows + p.rows - 1) / p.rows;
+    if (!p.tiled) {
+        attend_splits(B, Hkv, p.mtiles, max_len, &p.nsplit, &p.split);
+        return p;
+    }
     // One CTA a multiprocessor.  One round of them where two splits or more fit into
     // it, else three (uneven lengths even out); splits of four tiles at least.
-    if (max_len > (1 << 30)) max_len = 1 << 30;
-    const long long base = 1LL * B * Hkv * mtiles;
+    const long long base = 1LL * B * Hkv * p.mtiles;
     long long n = 148 / base;
     if (n < 2) n = (3 * 148 + base - 1) / base;
     long long len = (max_len + n - 1) / n;
     len = (len + 127) / 128 * 128;
     if (len < 512) len = 512;
     if (len > (1 << 30)) len = 1 << 30;
-    *nsplit = static_cast<int>((max_len + len - 1) / len);
-    *split = static_cast<int>(len);
+    p.nsplit = static_cast<int>((max_len + len - 1) / len);
+    p.split = static_cast<int>(len);
+    return p;
 }
 
 inline size_t attend_workspace(int B, int Hq, int Hkv, int T, int D, int max_len) {
-    int nsplit, split;
-    attend_plan(B, Hq, Hkv, T, max_len, &nsplit, &split);
-    return nsplit > 1 ? static_cast<size_t>(B) * Hq * T * nsplit * (D + 2) * 4 : 0;
+    const AttendPlan p = attend_plan(B, Hq, Hkv, T, max_len);
+    return p.nsplit > 1 ? static_cast<size_t>(B) * Hq * T * p.nsplit * (D + 2) * 4 : 0;
 }
 
 template <int D, bool BF16>
@@ -540,11 +557,11 @@ bool attend_set_attributes() {
 }
 
 template <int D, bool BF16>
-void attend_launch(const AttendParams& p, cudaStream_t st) {
+void attend_launch(const AttendPlan& plan, const AttendParams& p, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(p.mtiles) * p.nsplit * p.Hkv * p.B;
-    if (attend_tiled(p.Hq, p.Hkv, p.T))
+    if (plan.tiled)
         cache_attend_tile_kernel<D, BF16><<<grid, 640, AttendTileCfg<D>::SMEM, st>>>(p);
-    else if (attend_rows(p.Hq, p.Hkv, p.T) == 8)
+    else if (plan.rows == 8)
         cache_attend_kernel<D, BF16, 1><<<grid, 128, AttendCfg<D, 1>::SMEM, st>>>(p);
     else
         cache_attend_kernel<D, BF16, 2><<<grid, 128, AttendCfg<D, 2>::SMEM, st>>>(p);

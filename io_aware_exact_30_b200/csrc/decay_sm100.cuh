@@ -76,31 +76,32 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // OX_i is weighted with L^pos_i and Zh_j with scale L^(n - pos_j).
 //
 // The state is an fp32 result of its own, so Zh must not be rounded to the
-// 16-bit type: it goes to the tensor cores as two (fp16, 22 bits) or three (bf16,
-// 24 bits) 16-bit pieces, side by side in the N extent of one product with Y,
-// and the pieces' sums are added in fp32.  (One bf16 piece put 2e-3 on the state,
-// two 3e-6, three 2e-7, the fp32 sums' own.)  P, the copy of S that X meets and the
-// result are rounded to the 16-bit type, half a step each: they only reach the
-// 16-bit result.
+// 16-bit type (one bf16 piece of it would be off by up to 2^-8, two by 2^-16): it
+// goes to the tensor cores as two (fp16, 22 bits) or three (bf16, 24 bits) 16-bit
+// pieces, side by side in the N extent of one product with Y, and the pieces' sums
+// are added in fp32.  P, the copy of S that X meets and the result are rounded to
+// the 16-bit type, half a step each: they only reach the 16-bit result.
 //
-// Bound by the tensor pipe and its hand-overs at D = 128 (per chunk A 512, Y^T Zh
-// 768, X S and P Z 380 cycles each against 1300 for the chunk's share of HBM
-// bandwidth), by HBM at D = 64.
+// What bounds it: shared memory and the hand-overs.  At D = 128 a chunk's products
+// take about 2150 cycles of the tensor pipe, and the operands they read, the loads,
+// Zh, the state's copy and the staged result about 3100 cycles of shared-memory
+// bandwidth; the roles' chain makes 4700 of it (2.4 us a chunk).  HBM would allow 1.3 us.
+// Measured (one B200, device time): 4 x 16 heads of 4096 tokens, d = 128, bf16: 85 us
+// (269 MB and states: 3.2 TB/s), the gradients 232 us; 12 heads of 23400 tokens,
+// d = 64, fp16, in 12 segments: 70 us.  The same kernel without Zh, P and stores: 57 us.
 //
 // Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
-// products; 16 warps make P and the output (thread = token; each 32 keys of P and
-// 16 features); 4 hold the state (thread = feature of y); 8 make Zh (thread =
-// token, 32 features each).  Every role's work lies on the chain from one chunk to
-// the next (Zh is written when its last reader is done), so it is spread over as many
-// warps as the registers carry (8 + 4 + 4 warps: 103 us for the large-head
-// prompt where these take 87).  Registers are dealt out
-// between the warpgroups (setmaxnreg).  Issue order: A_0, then per chunk Y^T Zh, X S,
-// A of the next chunk, P Z: while the row warps read X S and hand over P, the
-// next A runs, and the next P is made during P Z and Y^T Zh.  Every product has a
-// completion barrier for either stage, on which all that depends on it waits, the
-// reload of its operand included: X, Y and Z are each reloaded as soon as their
-// last product is done, and each product is committed once.  (A second commit
-// behind the same products held the issuing thread for about 1200 cycles.)
+// products, warp 2 stores (TMA); 16 warps make P and the output (thread = token;
+// each 32 keys of P and 16 features); 4 hold the state (thread = feature of y); 8 make
+// Zh (thread = token, 32 features each).  Every role's work lies on the chain from
+// one chunk to the next (Zh is written when its last reader is done), so it is spread
+// over as many warps as the registers carry (8 row warps and 16 for Zh instead: 87.6
+// against 85.6 us for the large-head prompt).  Registers are dealt out between the warpgroups (setmaxnreg).
+// Issue order: A_0, then per chunk Y^T Zh, X S, A of the next chunk, P Z: while the
+// row warps read X S and hand over P, the next A runs, and the next P is made during
+// P Z and Y^T Zh.  Every product has a completion barrier for either stage, on which
+// all that depends on it waits, the reload of its operand included: X, Y and Z are
+// each reloaded as soon as their last product is done.
 //
 // STATE: only the segment's own contribution to the state (from zero).
 template <int D, bool BF16>
@@ -657,7 +658,8 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
 // Segments of a call: one, unless its CTAs (one per pass, head and 64 features)
 // fill less than half of the device's 148 multiprocessors; then as many as fit,
 // of four chunks at least (a segment costs a second pass over y and z, and a
-// state written and read).
+// state written and read: 12 heads of 23400 tokens, d = 64, take 70 us in 12
+// segments; 183 chunks in a row are 370 us at the 2 us each that a long walk takes).
 inline void decay_segments(int B, int H, int N, int d, int passes, int* nseg, int* seg_chunks) {
     const long long ctas = 1LL * passes * B * H * (d / 64);
     const int chunks = (N + kDecayChunk - 1) / kDecayChunk;
@@ -695,9 +697,11 @@ void decay_launch(const DecayMaps& maps, const DecayParams& p, cudaStream_t st) 
 }
 
 // One token: S <- g S + k v^T, o = scale q S, the state read and written once:
-// bound by HBM (8 D^2 bytes a head).  One CTA per head and slice of 4 COLS4
-// columns; a thread holds 4 columns of D / ROWS rows, all loaded before the first
-// is used; the ROWS partial sums of o meet in shared memory.
+// bound by HBM (8 D^2 bytes a head; 128 x 16 heads of D = 128: 41 us, 6.5 TB/s).  One
+// CTA per head and slice of 4 COLS4 columns (32: four CTAs a head at D = 128, so that a
+// single sequence's 16 heads reach 64 multiprocessors: 2.1 us, where one CTA a head and
+// a thread a column took 23); a thread holds 4 columns of D / ROWS rows, all loaded
+// before the first is used; the ROWS partial sums of o meet in shared memory.
 template <int D, bool BF16, int COLS4>
 __global__ void __launch_bounds__(256) decay_step_kernel(const void* q, const void* k, const void* v,
                                                          const float* log_decay, const float* in,
