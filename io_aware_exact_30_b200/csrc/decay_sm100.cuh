@@ -52,7 +52,8 @@ __device__ __forceinline__ int decay_len(const int* lens, int b, int N) {
 // log_decay -inf (no memory at all) times 0 would not be 0: held at -1e4,
 // whose exponential is 0.
 __device__ __forceinline__ float decay_log(const float* log_decay, int h) {
-    return fmaxf(log_decay[h], -1e4f);
+    const float x = log_decay[h];
+    return x < -1e4f ? -1e4f : x;  // NaN stays
 }
 
 constexpr int kDecayChunk = 128;
@@ -107,6 +108,9 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 template <int D, bool BF16>
 struct DecayCfg {
     static constexpr int NP = BF16 ? 3 : 2;             // pieces of Zh
+    // fp16's second piece is stored times 2^11, the first one's size, so that small
+    // values keep their bits (unscaled, terms of 1e-5 would be off by 1e-3)
+    static constexpr float PIECE_UP = BF16 ? 1.f : 2048.f;
     static constexpr uint32_t XB = D * 256u;            // X of a chunk
     static constexpr uint32_t YB = 32768u;              // Y; at D = 64 its upper half stays zero
     static constexpr uint32_t ZB = 16384u;              // 64 features of Z
@@ -513,7 +517,8 @@ __global__ void __launch_bounds__(1024, 1)
                     uint64_t sum = f2(__uint_as_float(v[NP - 1][2 * e]), __uint_as_float(v[NP - 1][2 * e + 1]));
 #pragma unroll
                     for (int k = NP - 2; k >= 0; --k)  // the small pieces first
-                        sum = add2(sum, f2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])));
+                        sum = fma2(sum, f2(1.f / C::PIECE_UP, 1.f / C::PIECE_UP),
+                                   f2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])));
                     uint64_t& x = st[8 * cc + e];
                     x = fma2(g, x, fma2(g2, x, sum));
                 }
@@ -571,6 +576,7 @@ __global__ void __launch_bounds__(1024, 1)
                             out[k][e] = pack2<BF16>(x.x, x.y);
                             const float2 h = unpack2<BF16>(out[k][e]);
                             f = fma2(f2(h.x, h.y), minus, f);
+                            if (!BF16) f = mul2(f, f2(C::PIECE_UP, C::PIECE_UP));
                         }
                     }
 #pragma unroll

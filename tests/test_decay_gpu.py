@@ -268,3 +268,31 @@ def test_large_heads_shape_and_repeatability():
         for x, y in zip(g[:3], ga):
             close(f64(x), f64(y[bi:bi + 1, h:h + 1]), 2 * half("bf16"), "grad")
         close(f64(g[3]), f64(ga[3][bi:bi + 1, h:h + 1]), 2 * STATE_TOL, "dstate")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_states_of_small_fp16_values(d):
+    """Values and gradients of about 1e-4, near fp16's smallest normal number: the
+    states, which are fp32, keep their precision."""
+    (q, k, v, do), _ = inputs(1, 3, 333, d, "fp16", 37)
+    v, do = v * 1e-4, do * 1e-4
+    ld = decays(3)
+    _, s1 = attn.decay_forward(q, k, v, ld)
+    ds = attn.decay_backward(q, k, v, ld, do)[3]
+    f = [f64(x) for x in (q, k, v, do)]
+    zero = np.zeros((1, 3, d, d))
+    _, want = ref.decay_forward(*f[:3], f64(ld), zero, [333], 1 / math.sqrt(d))
+    close(f64(s1), want, STATE_TOL, "state")
+    want = ref.decay_backward(*f[:3], f64(ld), f[3], zero, zero, [333], 1 / math.sqrt(d))[3]
+    close(f64(ds), want, STATE_TOL, "dstate")
+
+
+def test_a_decay_of_nan_is_not_hidden():
+    (q, k, v, do), (s0, ds) = inputs(1, 3, 140, 64, "bf16", 38)
+    ld = torch.tensor([-0.1, math.nan, -0.2], device="cuda")
+    o, s1 = attn.decay_forward(q, k, v, ld, state=s0)
+    grads = attn.decay_backward(q, k, v, ld, do, state=s0, dstate=ds)
+    step = attn.decay_step(*(x[:, :, :1].contiguous() for x in (q, k, v)), ld, s0)
+    assert attn.attn_last_device_status() == 0
+    for x in (o, s1, *grads, *step):
+        assert torch.isnan(x[:, 1]).all() and torch.isfinite(x[:, ::2]).all()
