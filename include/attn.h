@@ -252,7 +252,7 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * 16, 32, 64 or 128 tokens.  page_table: (B, max_pages) int32; the token of
  * sequence b at position t lies in slot t % page of page
  * page_table[b][t / page].  The cache may hold more than 2^31 codes; a
- * sequence's max_pages * page must stay below 2^31 tokens.  Codes and the
+ * sequence's max_pages * page is at most 2^30 tokens.  Codes and the
  * 16-bit tensors are 16-byte aligned, fp32 and int32 arrays 4-byte aligned, all
  * device memory of the current device.
  *
@@ -266,8 +266,8 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * round again.  What a page held before its first slot is written does not
  * matter (its scale included), so pages need no clearing when they are reused;
  * slots past the new tokens are not touched.  lens is not updated.  A page that
- * receives tokens must belong to one sequence only (two writers of one page
- * leave it undefined).
+ * receives tokens must stand once in the tables (two writers of one page leave
+ * it undefined); pages that are only read may be shared.
  *
  * attn_cache_attend: q (B, Hq, T, d), Hq a multiple of Hkv; query head h reads
  * key/value head h / (Hq / Hkv).  lens[b]: tokens sequence b holds, those of
@@ -277,7 +277,8 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * attn_fwd writes them; a query that sees no key gets O = 0 and lse = -inf;
  * rows t >= q_lens[b] are left as they were.  max_len: an upper bound of lens
  * that sizes the split of long sequences over the device (a larger one costs
- * time, a sequence longer than it is still attended to in full).  workspace:
+ * time, a sequence longer than it is still attended to in full).  Sums are fp32
+ * and divided at the end: o is finite for values up to 2^64.  workspace:
  * attn_cache_attend_workspace_bytes() bytes of the same sizes and max_len, 16-byte
  * aligned (may be NULL when that is 0); its contents on entry do not matter.
  *
@@ -336,8 +337,10 @@ int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned cha
  * attn_decay_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0); its
  * contents on entry do not matter.  Every sum is made in a fixed order: results
  * repeat bit for bit.  States are fp32 throughout (errors of about 2^-22); in the
- * chunked forms the 16-bit results see a state and the in-chunk weights rounded to
- * their type.  Errors as attn_fwd.
+ * chunked forms the 16-bit results see a state (times scale, forwards) and the
+ * in-chunk weights scale q.k g^distance rounded to their type: in fp16 those, and
+ * scale times an input, must stay within 65504, and the former lose relative
+ * precision below 2^-14 (bf16 has fp32's range).  A NaN in log_decay makes its head NaN.  Errors as attn_fwd.
  */
 size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward);
 

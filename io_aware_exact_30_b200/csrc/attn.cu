@@ -866,8 +866,8 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 int check_cache(int num_pages, int page, int max_pages, int Hkv) {
     if (page != 16 && page != 32 && page != 64 && page != 128) return ATTN_ERR_ARG;
     if (num_pages < 1 || max_pages < 1 || Hkv < 1) return ATTN_ERR_SHAPE;
-    // positions are 32-bit
-    if (1LL * max_pages * page >= (1LL << 31)) return ATTN_ERR_SHAPE;
+    // positions, rounded up to tiles, are 32-bit
+    if (1LL * max_pages * page > (1LL << 30)) return ATTN_ERR_SHAPE;
     return ATTN_OK;
 }
 

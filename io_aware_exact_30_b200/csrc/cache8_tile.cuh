@@ -14,8 +14,9 @@
 //
 // bf16 has fp32's range, so P needs no running maximum to stay in bounds: a row's
 // reference is the maximum of the first tile in which it sees a key, and one pass
-// over S does a tile.  Only when a score exceeds the reference by more than 2^60 is the
-// reference moved, O rescaled and the tile's pass repeated.  Keys 0-63 and 64-127 of
+// over S does a tile.  Only when a score exceeds the reference by more than 30 (log2: P
+// up to 2^30, so that 2^31 terms of |v| <= 2^64 stay in fp32) is the reference moved
+// and O rescaled.  Keys 0-63 and 64-127 of
 // the tiles are two softmaxes of their own, each with its reference, sum and output,
 // joined at the end: their warps never wait for one another.
 //
@@ -62,7 +63,7 @@ struct AttendTileCfg {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendParams p) {
     using C = AttendTileCfg<D>;
-    constexpr float kRaise = 60.f;
+    constexpr float kRaise = 30.f;
     constexpr int ROWS = 64;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw0 = smem_u32(smem_raw);

@@ -254,6 +254,21 @@ def test_attend_scores_that_climb_past_every_reference():
             check_attend(sign * q.abs(), cache, table, [n - 13])
 
 
+def test_attend_of_values_of_two_to_the_64():
+    """The largest values the sums are sized for, under scores that climb from tile to
+    tile by just less than moves a reference."""
+    page, d, n = 64, 128, 640
+    for Hq in (4, 40):
+        P, table = tables(1, n // page, 46)
+        cache = filled_cache(P, 1, page, d, 47)
+        cache.k.copy_(cache.k.float().abs().to(torch.float8_e4m3fn))
+        for i, pg in enumerate(table.cpu().long()[0]):
+            cache.k_scale[pg] = 2.0 ** (-9 + i / 2 // 1)
+            cache.v_scale[pg] = 2.0 ** 55  # codes to 448: 2^64
+        q = torch.randn(1, Hq, 1, d, generator=torch.Generator().manual_seed(48)).bfloat16().cuda()
+        check_attend(q.abs(), cache, table, [n])
+
+
 def test_attend_bad_pages_are_not_seen():
     page, d = 32, 64
     P, table = tables(4, 4, 17)

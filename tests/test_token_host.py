@@ -81,6 +81,12 @@ def test_decay_refusals():
     assert attn.strerror(-11) and attn.strerror(-11) != attn.strerror(-99)
 
 
+def test_cache_capacity_of_a_sequence():
+    """Positions, rounded up to a tile, stay 32-bit: at most 2^30 tokens a sequence."""
+    for call in (append, attend):
+        assert call(page=128, width=(1 << 23) + 1) == -2 and call(page=16, width=(1 << 26) + 1) == -2
+
+
 def test_workspace_sizes_of_invalid_calls_are_zero():
     assert attn.attn_cache_attend_workspace_bytes(1, 4, 3, 1, 64, 100) == 0
     assert attn.attn_cache_attend_workspace_bytes(1, 4, 2, 1, 96, 100) == 0
