@@ -9,6 +9,7 @@ library is missing or the device is not sm_100, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple
@@ -379,6 +380,7 @@ def attn_linear_fwd(q, k, v, o, workspace, scale: float | None = None, stream=No
 # Page sizes (tokens) of the 8-bit cache.
 PAGE_SIZES = (16, 32, 64, 128)
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32, _I32 = torch.float32, torch.int32
 
 
 class Cache8(NamedTuple):
@@ -429,21 +431,25 @@ def _optional(t, shape, dtype, name):
         raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor")
 
 
-def _cache_shape(cache, d, page_table, B):
+def _cache_shape(k, v, ks, vs, d, page_table, lens, B):
     """(num_pages, Hkv, page, max_pages) of a cache whose arrays fit together."""
-    k, v, ks, vs = cache
-    shape = k.shape
+    shape, code = k.shape, k.dtype
     if len(shape) != 4 or shape[3] != d or shape[2] not in PAGE_SIZES:
         raise ValueError(f"cache codes must be (num_pages, Hkv, page, {d}), page one of {PAGE_SIZES}")
-    if k.dtype not in _CODES:
+    P, H, page, _ = shape
+    if code not in _CODES:
         raise ValueError("cache codes must be float8_e4m3fn or uint8")
-    _alike(shape, k.dtype, (k, v), ("cache k", "cache v"))
-    _alike(shape[:2], torch.float32, (ks, vs), ("cache k_scale", "cache v_scale"))
+    if v.dtype is not code or v.shape != shape or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError(f"cache k and v must be contiguous with shape {tuple(shape)} and one dtype")
+    if ks.dtype is not _F32 or vs.dtype is not _F32 or ks.shape != (P, H) or vs.shape != (P, H) \
+            or not ks.is_contiguous() or not vs.is_contiguous():
+        raise ValueError(f"cache k_scale and v_scale must be contiguous float32 ({P}, {H}) tensors")
     table = page_table.shape
-    if page_table.dtype is not torch.int32 or len(table) != 2 or table[0] != B \
-            or not page_table.is_contiguous():
+    if page_table.dtype is not _I32 or len(table) != 2 or table[0] != B or not page_table.is_contiguous():
         raise ValueError(f"page_table must be a contiguous int32 ({B}, max_pages) tensor")
-    return shape[0], shape[1], shape[2], table[1]
+    if lens.dtype is not _I32 or lens.shape != (B,) or not lens.is_contiguous():
+        raise ValueError(f"lens must be a contiguous int32 ({B},) tensor")
+    return P, H, page, table[1]
 
 
 def _check_workspace(workspace, need):
@@ -458,18 +464,18 @@ def attn_cache_append(k, v, cache: Cache8, page_table, lens, n_new=None, stream=
     B, H, T, d = shape
     code = _dtype(k)
     _alike(shape, k.dtype, (k, v), ("k", "v"))
-    P, Hkv, page, width = _cache_shape(cache, d, page_table, B)
+    k8, v8, ks, vs = cache
+    P, Hkv, page, width = _cache_shape(k8, v8, ks, vs, d, page_table, lens, B)
     if H != Hkv:
         raise ValueError(f"k and v have {H} heads, the cache {Hkv}")
-    _alike((B,), torch.int32, (lens,), ("lens",))
     _optional(n_new, (B,), torch.int32, "n_new")
-    rc = lib().attn_cache_append(k.data_ptr(), v.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
-                                 cache[2].data_ptr(), cache[3].data_ptr(), page_table.data_ptr(),
-                                 lens.data_ptr(), _at(n_new), B, H, T, d, P, page, width, code,
-                                 _handle(k, stream))
+    rc = lib().attn_cache_append(k.data_ptr(), v.data_ptr(), k8.data_ptr(), v8.data_ptr(), ks.data_ptr(),
+                                 vs.data_ptr(), page_table.data_ptr(), lens.data_ptr(), _at(n_new), B, H,
+                                 T, d, P, page, width, code, _handle(k, stream))
     _check(rc, "attn_cache_append")
 
 
+@functools.lru_cache(maxsize=256)
 def attn_cache_attend_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, d: int, max_len: int) -> int:
     return int(lib().attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len))
 
@@ -490,24 +496,24 @@ def _attend(q, shape, cache, page_table, lens, o, lse, workspace, causal, scale,
     """attn_cache_attend with o and lse known to fit; workspace False: allocate it."""
     B, Hq, T, d = shape
     code = _dtype(q)
-    P, Hkv, page, width = _cache_shape(cache, d, page_table, B)
-    _alike((B,), torch.int32, (lens,), ("lens",))
+    k8, v8, ks, vs = cache
+    P, Hkv, page, width = _cache_shape(k8, v8, ks, vs, d, page_table, lens, B)
     _optional(q_lens, (B,), torch.int32, "q_lens")
     max_len = width * page if max_len is None else int(max_len)
-    need = lib().attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len)
+    need = attn_cache_attend_workspace_bytes(B, Hq, Hkv, T, d, max_len)
     if workspace is False:
         workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     else:
         _check_workspace(workspace, need)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = _lib.attn_cache_attend(q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
-                                cache[2].data_ptr(), cache[3].data_ptr(), page_table.data_ptr(),
-                                lens.data_ptr(), _at(q_lens), o.data_ptr(), lse.data_ptr(),
-                                _at(workspace), B, Hq, Hkv, T, d, P, page, width, max_len,
-                                1 if causal else 0, scale, code, _handle(q, stream))
+    rc = lib().attn_cache_attend(q.data_ptr(), k8.data_ptr(), v8.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                                 page_table.data_ptr(), lens.data_ptr(), _at(q_lens), o.data_ptr(),
+                                 lse.data_ptr(), _at(workspace), B, Hq, Hkv, T, d, P, page, width, max_len,
+                                 1 if causal else 0, scale, code, _handle(q, stream))
     _check(rc, "attn_cache_attend")
 
 
+@functools.lru_cache(maxsize=256)
 def attn_decay_workspace_bytes(B: int, H: int, N: int, d: int, backward: bool = False) -> int:
     return int(lib().attn_decay_workspace_bytes(B, H, N, d, int(bool(backward))))
 
@@ -524,11 +530,11 @@ def attn_decay_fwd(q, k, v, log_decay, o, state_in=None, state_out=None, lens=No
     _optional(state_in, (B, H, d, d), torch.float32, "state_in")
     _optional(state_out, (B, H, d, d), torch.float32, "state_out")
     _optional(lens, (B,), torch.int32, "lens")
-    _check_workspace(workspace, lib().attn_decay_workspace_bytes(B, H, N, d, 0))
+    _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = _lib.attn_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _at(state_in),
-                             _at(lens), o.data_ptr(), _at(state_out), _at(workspace), B, H, N, d, scale,
-                             code, _handle(q, stream))
+    rc = lib().attn_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _at(state_in),
+                              _at(lens), o.data_ptr(), _at(state_out), _at(workspace), B, H, N, d, scale,
+                              code, _handle(q, stream))
     _check(rc, "attn_decay_fwd")
 
 
@@ -546,12 +552,12 @@ def attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state_in=None, dstate_o
     _optional(dstate_out, (B, H, d, d), torch.float32, "dstate_out")
     _optional(dstate_in, (B, H, d, d), torch.float32, "dstate_in")
     _optional(lens, (B,), torch.int32, "lens")
-    _check_workspace(workspace, lib().attn_decay_workspace_bytes(B, H, N, d, 1))
+    _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d, True))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    rc = _lib.attn_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                             dout.data_ptr(), _at(state_in), _at(dstate_out), _at(lens), dq.data_ptr(),
-                             dk.data_ptr(), dv.data_ptr(), _at(dstate_in), _at(workspace), B, H, N, d,
-                             scale, code, _handle(q, stream))
+    rc = lib().attn_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                              dout.data_ptr(), _at(state_in), _at(dstate_out), _at(lens), dq.data_ptr(),
+                              dk.data_ptr(), dv.data_ptr(), _at(dstate_in), _at(workspace), B, H, N, d,
+                              scale, code, _handle(q, stream))
     _check(rc, "attn_decay_bwd")
 
 
@@ -565,7 +571,8 @@ def attn_decay_step(q, k, v, log_decay, state_in, o, state_out, scale: float | N
     code = _dtype(q)
     _alike(shape, q.dtype, (q, k, v, o), ("q", "k", "v", "o"))
     _alike((H,), torch.float32, (log_decay,), ("log_decay",))
-    _alike((B, H, d, d), torch.float32, (state_in, state_out), ("state_in", "state_out"))
+    _alike((B, H, d, d), torch.float32, (state_in,) if state_in is state_out else (state_in, state_out),
+           ("state_in", "state_out"))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     rc = lib().attn_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                state_in.data_ptr(), o.data_ptr(), state_out.data_ptr(), B, H, d, scale,
@@ -712,7 +719,8 @@ def cache_attend(q, cache: Cache8, page_table, lens, causal: bool = True, scale:
     shape = _shape(q)
     _alike(shape, q.dtype, (q,), ("q",))
     o = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
-    lse = q.new_empty(shape[:3], dtype=torch.float32)
+    B, Hq, T, _ = shape
+    lse = q.new_empty((B, Hq, T), dtype=torch.float32)
     if q_lens is not None:
         lse.fill_(-math.inf)
     _attend(q, shape, cache, page_table, lens, o, lse, False, causal, scale, q_lens, max_len, None)
@@ -725,7 +733,7 @@ def decay_forward(q, k, v, log_decay, scale: float | None = None, state=None, le
     B, H, N, d = _shape(q)
     o = torch.empty_like(q) if lens is None else torch.zeros_like(q)
     out = q.new_empty((B, H, d, d), dtype=torch.float32)
-    need = lib().attn_decay_workspace_bytes(B, H, N, d, 0)
+    need = attn_decay_workspace_bytes(B, H, N, d)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
     attn_decay_fwd(q, k, v, log_decay, o, state, out, lens, ws, scale)
     return o, out
@@ -742,7 +750,7 @@ def decay_backward(q, k, v, log_decay, dout, scale: float | None = None, state=N
     else:
         dq, dk, dv = q.new_zeros((3, B, H, N, d)).unbind()
     ds = q.new_empty((B, H, d, d), dtype=torch.float32)
-    need = lib().attn_decay_workspace_bytes(B, H, N, d, 1)
+    need = attn_decay_workspace_bytes(B, H, N, d, True)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
     attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state, dstate, ds, lens, ws, scale)
     return dq, dk, dv, ds
