@@ -89,7 +89,7 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // bandwidth; the roles' chain makes 4700 of it (2.4 us a chunk).  HBM would allow 1.3 us.
 // Measured (one B200, device time): 4 x 16 heads of 4096 tokens, d = 128, bf16: 85 us
 // (269 MB and states: 3.2 TB/s), the gradients 232 us; 12 heads of 23400 tokens,
-// d = 64, fp16, in 12 segments: 70 us.  The same kernel without Zh, P and stores: 57 us.
+// d = 64, fp16, in 12 segments: 66 us.  The same kernel without Zh, P and stores: 57 us.
 //
 // Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
 // products, warp 2 stores (TMA); 16 warps make P and the output (thread = token;
@@ -120,8 +120,8 @@ struct DecayCfg {
     // The result is staged for its TMA store in a buffer of its own or, where shared
     // memory is full (bf16, D = 128), in its step's Z, whose reload then waits for
     // the store (at D = 64 a buffer of its own takes a long prompt from 83 to 70 us;
-    // at D = 128 half of X's stage instead of Z's: forward 83.0 to 82.2, gradients
-    // 231 to 240 us).
+    // at D = 128 half of X's stage instead of Z's: forward 85.3 to 84.6, gradients
+    // 232 to 245 us).
     static constexpr bool OWN_O = D == 64 || !BF16;
     static constexpr uint32_t OFF_O = OWN_O ? OFF_S + D * 128u : XB + YB;
     static constexpr uint32_t O_STEP = OWN_O ? 0u : STAGE;
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(1024, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if constexpr (STATE) cudaTriggerProgrammaticLaunchCompletion();
     if (warp < 4) regs_down<C::R_ISSUE>();
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -461,6 +462,7 @@ __global__ void __launch_bounds__(1024, 1)
                 for (int c = 0; c < 32; ++c)
                     st[c] = f2(ps.init[mat + (hf * 64 + 2 * c) * D + a], ps.init[mat + (hf * 64 + 2 * c + 1) * D + a]);
             } else if (p.nseg > 1 || ps.init) {
+                if (p.nseg > 1) cudaGridDependencySynchronize();  // the scan's result, all else is the call's input
                 const float4* src = reinterpret_cast<const float4*>((p.nseg > 1 ? p.seg + seg_mat : ps.init + mat) +
                                                                     a * D + hf * 64);
 #pragma unroll
@@ -626,6 +628,7 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
     const size_t mat = static_cast<size_t>(bh) * PER;
     float4* at = reinterpret_cast<float4*>(p.seg) + static_cast<size_t>(pi) * p.nseg * p.B * p.H * PER + mat + e4;
     const size_t step = static_cast<size_t>(p.B) * p.H * PER;
+    cudaTriggerProgrammaticLaunchCompletion();
     const int whole = p.seg_chunks * kDecayChunk;  // tokens of a full segment
     const double full = exp(ld * whole);
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -638,6 +641,7 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
             S = reinterpret_cast<const float4*>(ps.init)[mat + e4];
         }
     }
+    cudaGridDependencySynchronize();  // the segments' own contributions
     for (int i0 = 0; i0 < p.nseg; i0 += AHEAD) {
         float4 own[AHEAD];
 #pragma unroll
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
 // Segments of a call: one, unless its CTAs (one per pass, head and 64 features)
 // fill less than half of the device's 148 multiprocessors; then as many as fit,
 // of four chunks at least (a segment costs a second pass over y and z, and a
-// state written and read: 12 heads of 23400 tokens, d = 64, take 70 us in 12
+// state written and read: 12 heads of 23400 tokens, d = 64, take 66 us in 12
 // segments; 183 chunks in a row are 370 us at the 2 us each that a long walk takes).
 inline void decay_segments(int B, int H, int N, int d, int passes, int* nseg, int* seg_chunks) {
     const long long ctas = 1LL * passes * B * H * (d / 64);
@@ -695,11 +699,23 @@ template <int D, bool BF16>
 void decay_launch(const DecayMaps& maps, const DecayParams& p, cudaStream_t st) {
     constexpr uint32_t bytes = DecayCfg<D, BF16>::SMEM_BYTES;
     const unsigned grid = static_cast<unsigned>(p.B) * p.H * (D / 64) * p.passes * p.nseg;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute early;  // a launch begins while the one before still runs (68 to 66 us)
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.stream = st;
     if (p.nseg > 1) {
         decay_chunk_kernel<D, BF16, true><<<grid, 1024, bytes, st>>>(maps, p);
-        decay_scan_kernel<D><<<dim3(D * D / 512, p.B * p.H, p.passes), 128, 0, st>>>(p);
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3(D * D / 512, p.B * p.H, p.passes);
+        cfg.blockDim = dim3(128);
+        cudaLaunchKernelEx(&cfg, decay_scan_kernel<D>, p);
     }
-    decay_chunk_kernel<D, BF16, false><<<grid, 1024, bytes, st>>>(maps, p);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchKernelEx(&cfg, decay_chunk_kernel<D, BF16, false>, maps, p);
 }
 
 // One token: S <- g S + k v^T, o = scale q S, the state read and written once:
