@@ -174,6 +174,21 @@ __global__ void __launch_bounds__(1024, 1)
     volatile uint32_t* abort_flag = tmem_slot + 1;
     float* pw = reinterpret_cast<float*>(gbase + C::OFF_PW) + 32;
     const double ld = decay_log(p.log_decay, bh % p.H);
+    // of step i: Y (what 0), X (1), Z (2)
+    auto load = [&](int i, int what) {
+        const int s = i & 1, row = chunk(i) * kDecayChunk;
+        const uint32_t sx = base + s * C::STAGE, sy = sx + C::XB, sz = sy + C::YB;
+        if (what == 2) {
+            mbar_arrive_expect_tx(DBAR(C::B_ZF + s), C::ZB);
+            tma_load_3d(sz, &maps.m[ps.z], DBAR(C::B_ZF + s), hf * 64, row, bh);
+        } else if (what == 0 || !STATE) {
+            const uint32_t bar = DBAR((what ? C::B_XF : C::B_YF) + s);
+            mbar_arrive_expect_tx(bar, D * 256u);
+#pragma unroll
+            for (int kb = 0; kb < HALVES; ++kb)
+                tma_load_3d((what ? sx : sy) + kb * 16384u, &maps.m[what ? ps.x : ps.y], bar, kb * 64, row, bh);
+        }
+    };
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
             const int rows = i == C::B_PF || i == C::B_OE || i >= C::B_OW;
@@ -182,6 +197,9 @@ __global__ void __launch_bounds__(1024, 1)
         }
         *abort_flag = 0u;
         fence_mbar_init();
+        // both stages are empty: their loads run while the tables are made
+        for (int i = 0; i < 2 && i < nch; ++i)
+            for (int what = 0; what < 3; ++what) load(i, what);
     }
     // L^m; the product's rounding error enters as a correction, so a power's error
     // stays that of the exponential
@@ -209,32 +227,19 @@ __global__ void __launch_bounds__(1024, 1)
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (elect_one()) {
-            const CUtensorMap *mx = &maps.m[ps.x], *my = &maps.m[ps.y], *mz = &maps.m[ps.z];
             bool ok = true;
-            int issued = 0;
-            for (int i = 0; i < nch; ++i) {
-                const int s = i & 1, row = chunk(i) * kDecayChunk;
+            int issued = 3 * min(nch, 2);
+            for (int i = 2; i < nch; ++i) {
+                const int s = i & 1;
                 const uint32_t par = ((i >> 1) - 1) & 1;
-                const uint32_t sx = base + s * C::STAGE, sy = sx + C::XB, sz = sy + C::YB;
-                if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_KVF + s), par, abort_flag))) break;
-                mbar_arrive_expect_tx(DBAR(C::B_YF + s), D * 256u);
-#pragma unroll
-                for (int kb = 0; kb < HALVES; ++kb)
-                    tma_load_3d(sy + kb * 16384u, my, DBAR(C::B_YF + s), kb * 64, row, bh);
+                if (!(ok = wait_bounded(DBAR(C::B_KVF + s), par, abort_flag))) break;
+                load(i, 0);
                 issued = 3 * i + 1;
-                if constexpr (!STATE) {
-                    if (i >= 2 && !(ok = wait_bounded(DBAR(C::B_QSD + s), par, abort_flag))) break;
-                    mbar_arrive_expect_tx(DBAR(C::B_XF + s), D * 256u);
-#pragma unroll
-                    for (int kb = 0; kb < HALVES; ++kb)
-                        tma_load_3d(sx + kb * 16384u, mx, DBAR(C::B_XF + s), kb * 64, row, bh);
-                }
+                if (!STATE && !(ok = wait_bounded(DBAR(C::B_QSD + s), par, abort_flag))) break;
+                load(i, 1);
                 issued = 3 * i + 2;
-                if (!STATE && i >= 2 &&
-                    !(ok = wait_bounded(DBAR((C::OWN_O ? C::B_OD : C::B_OR) + s), par, abort_flag)))
-                    break;
-                mbar_arrive_expect_tx(DBAR(C::B_ZF + s), C::ZB);
-                tma_load_3d(sz, mz, DBAR(C::B_ZF + s), hf * 64, row, bh);
+                if (!STATE && !(ok = wait_bounded(DBAR((C::OWN_O ? C::B_OD : C::B_OR) + s), par, abort_flag))) break;
+                load(i, 2);
                 issued = 3 * i + 3;
             }
             if (!ok) {  // let the copies in flight land before the CTA exits
