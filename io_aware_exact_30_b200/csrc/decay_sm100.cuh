@@ -88,8 +88,8 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // Zh, the state's copy and the staged result about 3100 cycles of shared-memory
 // bandwidth; the roles' chain makes 4700 of it (2.4 us a chunk).  HBM would allow 1.3 us.
 // Measured (one B200, device time): 4 x 16 heads of 4096 tokens, d = 128, bf16: 85 us
-// (269 MB and states: 3.2 TB/s), the gradients 232 us; 12 heads of 23400 tokens,
-// d = 64, fp16, in 12 segments: 66 us.  The same kernel without Zh, P and stores: 57 us.
+// (269 MB and states: 3.2 TB/s), the gradients 235 us; 12 heads of 23400 tokens,
+// d = 64, fp16, in 12 segments: 63 us.  The same kernel without Zh, P and stores: 57 us.
 //
 // Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
 // products, warp 2 stores (TMA); 16 warps make P and the output (thread = token;
@@ -351,9 +351,36 @@ __global__ void __launch_bounds__(1024, 1)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float* near = rev ? pw : pw + 132;
         const bool steep = pw[31] < 0x1p-100f;  // L^-31 out of range
+        uint32_t o16[8] = {};  // the output of a step, until it is staged
+        auto stage = [&](int i) -> bool {
+            const int b = i & 1, n = tokens(i);
+            // the staging's previous content has left
+            if (C::OWN_O && i >= 1 &&
+                !__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OR + (b ^ 1)), ((i - 1) >> 1) & 1, abort_flag)))
+                return false;
+            if (n == kDecayChunk) {
+                // as the TMA store expects it: 16-byte piece j of row r at j ^ (r mod 8).
+                // Stored from registers, 32 bytes of each row by a thread, every store was
+                // 32 wavefronts of L1: 31 of the large-head prompt's 103 us.
+                uint8_t* dst = gbase + C::OFF_O + b * C::O_STEP + r * 128;
+                *reinterpret_cast<uint4*>(dst + (((2 * cb) ^ (r & 7)) << 4)) = make_uint4(o16[0], o16[1], o16[2], o16[3]);
+                *reinterpret_cast<uint4*>(dst + (((2 * cb + 1) ^ (r & 7)) << 4)) =
+                    make_uint4(o16[4], o16[5], o16[6], o16[7]);
+                fence_proxy_async_smem();
+            } else if (r < n) {  // rows past the sequence's end stay as they are
+                uint4* dst = reinterpret_cast<uint4*>(
+                    static_cast<uint8_t*>(ps.out) +
+                    (static_cast<size_t>(bh) * p.N + chunk(i) * kDecayChunk + r) * (D * 2) + hf * 128 + cb * 32);
+                dst[0] = make_uint4(o16[0], o16[1], o16[2], o16[3]);
+                dst[1] = make_uint4(o16[4], o16[5], o16[6], o16[7]);
+            }
+            mbar_arrive(DBAR(C::B_OW + b));
+            return true;
+        };
+        bool ok = true;
         for (int i = 0; !STATE && i < nch; ++i) {
             const int b = i & 1, n = tokens(i);
-            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_AF + b), (i >> 1) & 1, abort_flag))) break;
+            if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_AF + b), (i >> 1) & 1, abort_flag)))) break;
             tc_fence_after();
             {
                 const uint32_t col = lane_addr + 128u * b + 32u * cb;
@@ -405,7 +432,7 @@ __global__ void __launch_bounds__(1024, 1)
                 tmem_st_wait();
             }
             // X S, before P Z takes its columns
-            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD + b), (i >> 1) & 1, abort_flag))) break;
+            if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD + b), (i >> 1) & 1, abort_flag)))) break;
             tc_fence_after();
             uint32_t ox[16], v[16];
             tmem_ld16(lane_addr + C::COL_O + 16u * cb, ox);
@@ -414,7 +441,10 @@ __global__ void __launch_bounds__(1024, 1)
             for (int e = 0; e < 16; ++e) reg_fence(ox[e]);
             tc_fence_before();
             mbar_arrive(DBAR(C::B_PF));
-            if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OD + b), (i >> 1) & 1, abort_flag))) break;
+            // in a buffer of its own the previous step's output is staged during P Z
+            // (12 heads of 23400 tokens: 64.2 to 62.9 us)
+            if (C::OWN_O && i >= 1 && !(ok = stage(i - 1))) break;
+            if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OD + b), (i >> 1) & 1, abort_flag)))) break;
             tc_fence_after();
             tmem_ld16(lane_addr + C::COL_O + 16u * cb, v);
             tmem_ld_wait();
@@ -423,33 +453,13 @@ __global__ void __launch_bounds__(1024, 1)
             tc_fence_before();
             mbar_arrive(DBAR(C::B_OE));
             const float w = r < n ? (rev ? pw[n - 1 - r] : pw[r + 1]) : 0.f;
-            uint32_t o16[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
                                      fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
-            // the staging's previous content has left
-            if (C::OWN_O && i >= 1 &&
-                !__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OR + (b ^ 1)), ((i - 1) >> 1) & 1, abort_flag)))
-                break;
-            if (n == kDecayChunk) {
-                // as the TMA store expects it: 16-byte piece j of row r at j ^ (r mod 8).
-                // Stored from registers, 32 bytes of each row by a thread, every store was
-                // 32 wavefronts of L1: 31 of the large-head prompt's 103 us.
-                uint8_t* dst = gbase + C::OFF_O + b * C::O_STEP + r * 128;
-                *reinterpret_cast<uint4*>(dst + (((2 * cb) ^ (r & 7)) << 4)) = make_uint4(o16[0], o16[1], o16[2], o16[3]);
-                *reinterpret_cast<uint4*>(dst + (((2 * cb + 1) ^ (r & 7)) << 4)) =
-                    make_uint4(o16[4], o16[5], o16[6], o16[7]);
-                fence_proxy_async_smem();
-            } else if (r < n) {  // rows past the sequence's end stay as they are
-                uint4* dst = reinterpret_cast<uint4*>(
-                    static_cast<uint8_t*>(ps.out) +
-                    (static_cast<size_t>(bh) * p.N + chunk(i) * kDecayChunk + r) * (D * 2) + hf * 128 + cb * 32);
-                dst[0] = make_uint4(o16[0], o16[1], o16[2], o16[3]);
-                dst[1] = make_uint4(o16[4], o16[5], o16[6], o16[7]);
-            }
-            mbar_arrive(DBAR(C::B_OW + b));
+            if (!C::OWN_O && !(ok = stage(i))) break;
         }
+        if (C::OWN_O && !STATE && ok && nch > 0) stage(nch - 1);
     } else if (warp < 24) {
         // -------------------------------------------------------- the state
         regs_up<C::R_STATE>();
@@ -673,7 +683,7 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
 // Segments of a call: one, unless its CTAs (one per pass, head and 64 features)
 // fill less than half of the device's 148 multiprocessors; then as many as fit,
 // of four chunks at least (a segment costs a second pass over y and z, and a
-// state written and read: 12 heads of 23400 tokens, d = 64, take 66 us in 12
+// state written and read: 12 heads of 23400 tokens, d = 64, take 63 us in 12
 // segments; 183 chunks in a row are 370 us at the 2 us each that a long walk takes).
 inline void decay_segments(int B, int H, int N, int d, int passes, int* nseg, int* seg_chunks) {
     const long long ctas = 1LL * passes * B * H * (d / 64);

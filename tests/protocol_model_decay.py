@@ -152,17 +152,8 @@ def store(nc, v):
 
 
 def rows(r, nc, v):
-    for i in range(nc):
-        s, u = i & 1, i >> 1
-        yield from waits(v, ("af", f"AF{s}", u, True))
-        yield ("read", ("A", s, r), ("A", i))
-        yield ("write", ("A", s, r), ("P", i))
-        yield from waits(v, ("qsd", f"QSD{s}", u, True))
-        yield ("read", ("O", r), ("OX", i))
-        yield ("arrive", "PF", i)
-        yield from waits(v, ("od", f"OD{s}", u, True))
-        yield ("read", ("O", r), ("O", i))
-        yield ("arrive", "OE", i)
+    def stage(i):
+        s = i & 1
         if v.own_o:
             yield from waits(v, ("stage_free", f"OR{s ^ 1}", (i - 1) >> 1, i >= 1))
         if v.partial != i:
@@ -174,6 +165,24 @@ def rows(r, nc, v):
                 yield ("write", ("ZO", s, r), i)
                 yield ("write", ("Z", s), ("staged", i))
         yield ("arrive", *ow(i, v))
+
+    for i in range(nc):
+        s, u = i & 1, i >> 1
+        yield from waits(v, ("af", f"AF{s}", u, True))
+        yield ("read", ("A", s, r), ("A", i))
+        yield ("write", ("A", s, r), ("P", i))
+        yield from waits(v, ("qsd", f"QSD{s}", u, True))
+        yield ("read", ("O", r), ("OX", i))
+        yield ("arrive", "PF", i)
+        if v.own_o and i >= 1:
+            yield from stage(i - 1)
+        yield from waits(v, ("od", f"OD{s}", u, True))
+        yield ("read", ("O", r), ("O", i))
+        yield ("arrive", "OE", i)
+        if not v.own_o:
+            yield from stage(i)
+    if v.own_o and nc:
+        yield from stage(nc - 1)
 
 
 def state(a, nc, v):
