@@ -318,8 +318,9 @@ int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned cha
  * (B, H, d, d) fp32, S[a][c] = feature a of k, feature c of v.  All device
  * memory of the current device, 16-byte aligned (log_decay and lens 4-byte).
  * lens: NULL, or (B) int32 tokens of each sequence (clamped to 0 .. N): rows
- * past it are neither read into a result nor written; a sequence of length 0
- * hands its state on unchanged.
+ * past it are not read into a result, and those of o, dq, dk and dv are written
+ * as zeros (zero_past != 0) or left as they were; a sequence of length 0 hands its
+ * state on unchanged.
  *
  * attn_decay_fwd: the chunked form, for whole prompts and training.  state_in
  * and state_out may each be NULL and may be the same array.
@@ -346,14 +347,14 @@ size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward);
 
 int attn_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay,
                    const float* state_in, const int* lens, void* o, float* state_out,
-                   void* workspace, int B, int H, int N, int d, float scale, attn_dtype_t dtype,
-                   void* stream);
+                   void* workspace, int B, int H, int N, int d, int zero_past, float scale,
+                   attn_dtype_t dtype, void* stream);
 
 int attn_decay_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                    const void* dout, const float* state_in, const float* dstate_out,
                    const int* lens, void* dq, void* dk, void* dv, float* dstate_in,
-                   void* workspace, int B, int H, int N, int d, float scale, attn_dtype_t dtype,
-                   void* stream);
+                   void* workspace, int B, int H, int N, int d, int zero_past, float scale,
+                   attn_dtype_t dtype, void* stream);
 
 int attn_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                     const float* state_in, void* o, float* state_out, int B, int H, int d,

@@ -93,9 +93,9 @@ def lib() -> ctypes.CDLL:
         L.attn_cache_attend.restype = ci
         L.attn_decay_workspace_bytes.argtypes = [ci] * 5
         L.attn_decay_workspace_bytes.restype = sz
-        L.attn_decay_fwd.argtypes = [vp] * 9 + [ci] * 4 + [cf, ci, vp]
+        L.attn_decay_fwd.argtypes = [vp] * 9 + [ci] * 5 + [cf, ci, vp]
         L.attn_decay_fwd.restype = ci
-        L.attn_decay_bwd.argtypes = [vp] * 13 + [ci] * 4 + [cf, ci, vp]
+        L.attn_decay_bwd.argtypes = [vp] * 13 + [ci] * 5 + [cf, ci, vp]
         L.attn_decay_bwd.restype = ci
         L.attn_decay_step.argtypes = [vp] * 7 + [ci] * 3 + [cf, ci, vp]
         L.attn_decay_step.restype = ci
@@ -519,9 +519,9 @@ def attn_decay_workspace_bytes(B: int, H: int, N: int, d: int, backward: bool = 
 
 
 def attn_decay_fwd(q, k, v, log_decay, o, state_in=None, state_out=None, lens=None, workspace=None,
-                   scale: float | None = None, stream=None) -> None:
+                   scale: float | None = None, stream=None, zero_past: bool = False) -> None:
     """O, state_out <- linear attention with a decay for each head, from state_in
-    (None: zeros); rows of o past lens[b] are left as they were."""
+    (None: zeros); rows of o past lens[b] are written as zeros or left as they were."""
     shape = _shape(q)
     B, H, N, d = shape
     code = _dtype(q)
@@ -533,16 +533,16 @@ def attn_decay_fwd(q, k, v, log_decay, o, state_in=None, state_out=None, lens=No
     _check_workspace(workspace, attn_decay_workspace_bytes(B, H, N, d))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     rc = lib().attn_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _at(state_in),
-                              _at(lens), o.data_ptr(), _at(state_out), _at(workspace), B, H, N, d, scale,
-                              code, _handle(q, stream))
+                              _at(lens), o.data_ptr(), _at(state_out), _at(workspace), B, H, N, d,
+                              1 if zero_past else 0, scale, code, _handle(q, stream))
     _check(rc, "attn_decay_fwd")
 
 
 def attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state_in=None, dstate_out=None,
                    dstate_in=None, lens=None, workspace=None, scale: float | None = None,
-                   stream=None) -> None:
+                   stream=None, zero_past: bool = False) -> None:
     """dQ, dK, dV, dstate_in <- gradients of sum(O * dout) + sum(state_out *
-    dstate_out); rows past lens[b] are left as they were."""
+    dstate_out); rows past lens[b] are written as zeros or left as they were."""
     shape = _shape(q)
     B, H, N, d = shape
     code = _dtype(q)
@@ -557,7 +557,7 @@ def attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state_in=None, dstate_o
     rc = lib().attn_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                               dout.data_ptr(), _at(state_in), _at(dstate_out), _at(lens), dq.data_ptr(),
                               dk.data_ptr(), dv.data_ptr(), _at(dstate_in), _at(workspace), B, H, N, d,
-                              scale, code, _handle(q, stream))
+                              1 if zero_past else 0, scale, code, _handle(q, stream))
     _check(rc, "attn_decay_bwd")
 
 
@@ -731,11 +731,11 @@ def decay_forward(q, k, v, log_decay, scale: float | None = None, state=None, le
     """Allocates O, the state and the workspace and runs attn_decay_fwd; returns
     (o, state after the last token).  Rows past lens[b] are 0."""
     B, H, N, d = _shape(q)
-    o = torch.empty_like(q) if lens is None else torch.zeros_like(q)
+    o = torch.empty_like(q)
     out = q.new_empty((B, H, d, d), dtype=torch.float32)
     need = attn_decay_workspace_bytes(B, H, N, d)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
-    attn_decay_fwd(q, k, v, log_decay, o, state, out, lens, ws, scale)
+    attn_decay_fwd(q, k, v, log_decay, o, state, out, lens, ws, scale, zero_past=True)
     return o, out
 
 
@@ -745,14 +745,11 @@ def decay_backward(q, k, v, log_decay, dout, scale: float | None = None, state=N
     (dq, dk, dv, gradient of the state before the first token).  Rows past
     lens[b] are 0."""
     B, H, N, d = _shape(q)
-    if lens is None:
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    else:
-        dq, dk, dv = q.new_zeros((3, B, H, N, d)).unbind()
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds = q.new_empty((B, H, d, d), dtype=torch.float32)
     need = attn_decay_workspace_bytes(B, H, N, d, True)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
-    attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state, dstate, ds, lens, ws, scale)
+    attn_decay_bwd(q, k, v, log_decay, dout, dq, dk, dv, state, dstate, ds, lens, ws, scale, zero_past=True)
     return dq, dk, dv, ds
 
 

@@ -1037,8 +1037,8 @@ extern "C" size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int bac
 
 extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay,
                               const float* state_in, const int* lens, void* o, float* state_out,
-                              void* workspace, int B, int H, int N, int d, float scale,
-                              attn_dtype_t dtype, void* stream) {
+                              void* workspace, int B, int H, int N, int d, int zero_past,
+                              float scale, attn_dtype_t dtype, void* stream) {
     const void* req[] = {q, k, v, o};
     const void* opt[] = {state_in, state_out, workspace};
     if (!log_decay) return ATTN_ERR_NULL;
@@ -1053,14 +1053,15 @@ extern "C" int attn_decay_fwd(const void* q, const void* k, const void* v, const
     p.pass[0] = {0, 1, 2, 3, o, state_in, state_out, 0, 0};
     p.log_decay = log_decay, p.lens = lens;
     p.passes = 1, p.B = B, p.H = H, p.N = N, p.scale = scale;
+    p.zero_past = zero_past ? 1 : 0;
     return launch_decay(req, 4, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                               const void* dout, const float* state_in, const float* dstate_out,
                               const int* lens, void* dq, void* dk, void* dv, float* dstate_in,
-                              void* workspace, int B, int H, int N, int d, float scale,
-                              attn_dtype_t dtype, void* stream) {
+                              void* workspace, int B, int H, int N, int d, int zero_past,
+                              float scale, attn_dtype_t dtype, void* stream) {
     const void* req[] = {q, k, v, dout, dq, dk, dv};
     const void* opt[] = {state_in, dstate_out, dstate_in, workspace};
     if (!log_decay) return ATTN_ERR_NULL;
@@ -1080,6 +1081,7 @@ extern "C" int attn_decay_bwd(const void* q, const void* k, const void* v, const
     p.pass[2] = {1, 0, 3, 6, dv, dstate_out, dstate_in, 0, 1};
     p.log_decay = log_decay, p.lens = lens;
     p.passes = 3, p.B = B, p.H = H, p.N = N, p.scale = scale;
+    p.zero_past = zero_past ? 1 : 0;
     return launch_decay(req, 7, p, d, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 

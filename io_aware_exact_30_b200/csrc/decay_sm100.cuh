@@ -36,6 +36,7 @@ struct DecayParams {
     float* seg;              // (passes, nseg, B H, D, D): states of the segments
     int passes, B, H, N;
     int nseg, seg_chunks;    // a sequence's chunks in segments of seg_chunks
+    int zero_past;           // the result's rows past a sequence's end: zeros, else untouched
     float scale;
 };
 
@@ -88,11 +89,11 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // Zh, the state's copy and the staged result about 3100 cycles of shared-memory
 // bandwidth; the roles' chain makes 4700 of it (2.4 us a chunk).  HBM would allow 1.3 us.
 // Measured (one B200, device time): 4 x 16 heads of 4096 tokens, d = 128, bf16: 85 us
-// (269 MB and states: 3.2 TB/s), the gradients 235 us; 12 heads of 23400 tokens,
-// d = 64, fp16, in 12 segments: 63 us.  The same kernel without Zh, P and stores: 57 us.
+// (269 MB and states: 3.2 TB/s), the gradients 236 us; 12 heads of 23400 tokens,
+// d = 64, fp16, in 12 segments: 64 us.  The same kernel without Zh, P and stores: 57 us.
 //
 // Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
-// products, warp 2 stores (TMA); 16 warps make P and the output (thread = token;
+// products, warp 2 stores (TMA), 3 fills rows past the end; 16 warps make P and the output (thread = token;
 // each 32 keys of P and 16 features); 4 hold the state (thread = feature of y); 8 make
 // Zh (thread = token, 32 features each).  Every role's work lies on the chain from
 // one chunk to the next (Zh is written when its last reader is done), so it is spread
@@ -343,6 +344,17 @@ __global__ void __launch_bounds__(1024, 1)
         }
         __syncwarp();
     } else if (warp < 4) {
+        // the rows of this segment past the sequence's end, if they are to be zeros (a
+        // fill of its own in front of the call: 54 us instead of 43 for the gradients of
+        // 8 x 12 heads to 1024 tokens)
+        if (!STATE && p.zero_past) {
+            const int whole = p.seg_chunks * kDecayChunk;
+            const int end = min(p.N - seg * whole, whole);
+            uint8_t* out = static_cast<uint8_t*>(ps.out) +
+                           (static_cast<size_t>(bh) * p.N + seg * whole) * (D * 2) + hf * 128 + (lane & 7) * 16;
+            for (int r = max(len - seg * whole, 0) + (lane >> 3); r < end; r += 4)
+                *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * (D * 2)) = make_uint4(0u, 0u, 0u, 0u);
+        }
     } else if (warp < 20) {
         // ----------------------------------------- P and the output (rows)
         regs_down<C::R_ROW>();
@@ -683,7 +695,7 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
 // Segments of a call: one, unless its CTAs (one per pass, head and 64 features)
 // fill less than half of the device's 148 multiprocessors; then as many as fit,
 // of four chunks at least (a segment costs a second pass over y and z, and a
-// state written and read: 12 heads of 23400 tokens, d = 64, take 63 us in 12
+// state written and read: 12 heads of 23400 tokens, d = 64, take 64 us in 12
 // segments; 183 chunks in a row are 370 us at the 2 us each that a long walk takes).
 inline void decay_segments(int B, int H, int N, int d, int passes, int* nseg, int* seg_chunks) {
     const long long ctas = 1LL * passes * B * H * (d / 64);

@@ -296,3 +296,27 @@ def test_a_decay_of_nan_is_not_hidden():
     assert attn.attn_last_device_status() == 0
     for x in (o, s1, *grads, *step):
         assert torch.isnan(x[:, 1]).all() and torch.isfinite(x[:, ::2]).all()
+
+
+@pytest.mark.parametrize("B,H,N,d,lens", [(3, 2, 300, 64, [0, 129, 256]), (2, 1, 2000, 128, [1, 700]),
+                                          (2, 20, 130, 128, [128, 37])])
+def test_rows_past_the_end_of_padded_batches(B, H, N, d, lens):
+    """The conveniences return zeros there (one and several segments), whatever the
+    memory held; the rest is what the call that leaves them alone writes."""
+    (q, k, v, do), (s0, ds) = inputs(B, H, N, d, "bf16", 39)
+    ld = decays(H)
+    junk = [torch.full_like(q, 7.0) for _ in range(6)]
+    o = torch.full_like(q, 7.0)
+    g = [torch.full_like(q, 7.0) for _ in range(3)]
+    ws = [torch.empty(max(attn.attn_decay_workspace_bytes(B, H, N, d, bw), 16), dtype=torch.uint8, device="cuda")
+          for bw in (False, True)]
+    attn.attn_decay_fwd(q, k, v, ld, o, s0, None, ints(lens), ws[0])
+    attn.attn_decay_bwd(q, k, v, ld, do, *g, s0, ds, None, ints(lens), ws[1])
+    del junk
+    got = [attn.decay_forward(q, k, v, ld, state=s0, lens=ints(lens))[0],
+           *attn.decay_backward(q, k, v, ld, do, state=s0, dstate=ds, lens=ints(lens))[:3]]
+    assert attn.attn_last_device_status() == 0
+    for a, b in zip(got, (o, *g)):
+        for i, n in enumerate(lens):
+            assert torch.equal(a[i, :, :n], b[i, :, :n])
+            assert (a[i, :, n:] == 0).all() and (b[i, :, n:] == 7).all()

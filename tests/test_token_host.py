@@ -29,12 +29,12 @@ def at(i):
 
 
 def fwd(p=P, B=2, H=2, N=5, d=64, scale=0.1, dt=0, q=None, ld=P, st=P, o=at(1)):
-    return attn.lib().attn_decay_fwd(q or p, p, p, ld, st, None, p and o, st, p, B, H, N, d, scale, dt, None)
+    return attn.lib().attn_decay_fwd(q or p, p, p, ld, st, None, p and o, st, p, B, H, N, d, 0, scale, dt, None)
 
 
 def bwd(p=P, B=2, H=2, N=5, d=64, scale=0.1, dt=0, q=None, ld=P, ds=ctypes.c_void_p(512), g=(at(1), at(2), at(3))):
     return attn.lib().attn_decay_bwd(q or p, p, p, ld, p, p, p, None, *(p and x for x in g), ds, p, B, H, N, d,
-                                     scale, dt, None)
+                                     0, scale, dt, None)
 
 
 def step(p=P, B=2, H=2, d=64, scale=0.1, dt=0, q=None, ld=P, o=at(1)):
