@@ -320,3 +320,37 @@ def test_rows_past_the_end_of_padded_batches(B, H, N, d, lens):
         for i, n in enumerate(lens):
             assert torch.equal(a[i, :, :n], b[i, :, :n])
             assert (a[i, :, n:] == 0).all() and (b[i, :, n:] == 7).all()
+
+
+def test_segmented_calls_back_to_back_in_a_graph():
+    """Calls of several segments, whose launches overlap, one after another on the same
+    workspace and the same state, eager and as a replayed graph."""
+    B, H, N, d = 1, 2, 1600, 64
+    ld = decays(H)
+    xs = [inputs(B, H, N, d, "bf16", 40 + i)[0][:3] for i in range(3)]
+    need = attn.attn_decay_workspace_bytes(B, H, N, d)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want, state = [], torch.zeros(B, H, d, d, device="cuda")
+    for x in xs:
+        o, state = attn.decay_forward(*x, ld, state=state)
+        want.append(o)
+        torch.cuda.synchronize()
+    out, s = [torch.empty_like(x[0]) for x in xs], torch.zeros(B, H, d, d, device="cuda")
+
+    def chain():
+        s.zero_()
+        for x, o in zip(xs, out):
+            attn.attn_decay_fwd(*x, ld, o, s, s, None, ws)
+
+    chain()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for again in range(3):
+        if again:
+            for o in out:
+                o.fill_(7.0)
+            graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(s, state)
+    assert attn.attn_last_device_status() == 0
