@@ -91,8 +91,10 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NBAR; ++i)
-            mbar_init(ABAR(i), i < C::B_SF || i == C::B_PF || i == C::B_PF + 1 || i == C::B_XF ? 256 : (i == C::B_QF ? 128 : 1));
+        for (int i = 0; i < C::NBAR; ++i) {
+            const bool all = i < C::B_SF || i == C::B_PF || i == C::B_PF + 1 || i == C::B_XF;
+            mbar_init(ABAR(i), all ? 256 : (i == C::B_QF ? 128 : 1));
+        }
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -141,8 +143,8 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
             for (int j = 0; ok && j < nt; ++j) {
                 const int s = j & 1;
                 if (j + 1 < nt && !(ok = issue_s(j + 1))) break;
-                if (!(ok = wait3(ABAR(C::B_PF + s), (j >> 1) & 1, true, ABAR(C::B_VF + s), (j >> 1) & 1, true, 0u, 0u, false,
-                                 abort_flag)))
+                if (!(ok = wait3(ABAR(C::B_PF + s), (j >> 1) & 1, true, ABAR(C::B_VF + s), (j >> 1) & 1, true, 0u, 0u,
+                                 false, abort_flag)))
                     break;
                 tc_fence_after();
 #pragma unroll

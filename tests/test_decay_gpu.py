@@ -6,9 +6,9 @@ type (the in-chunk weights, the state's copy for the tensor cores, the result),
 each uniform within half a step eps/2 and so eps/2/sqrt(3) in L2; three independent
 ones make eps/2.  A head of few tokens has too few roundings to average: the weight of
 a single token is one number, its rounding, up to eps/2, is the whole row's, and the
-result's own comes on top, so there each of the three counts in full, 3 eps/2.  States are fp32; their terms reach the tensor cores in two 16-bit
-pieces (2^-16 of a term at most for bf16), and fp32 sums of n terms add about
-sqrt(n) 2^-24: 2e-5.  A step rounds its result once and its state by a few 2^-24.
+result's own comes on top, so there each of the three counts in full, 3 eps/2.  States
+are fp32; their terms reach the tensor cores in 16-bit pieces (2^-16 of a term at most),
+and fp32 sums of n terms add about sqrt(n) 2^-24: 2e-5.  A step rounds its result once and its state by a few 2^-24.
 """
 
 import math
