@@ -263,7 +263,8 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * was larger and the page held tokens of this sequence before (slot 0 < fill);
  * codes are e4m3(x / s), nearest even.  When the scale of a page grows, the held
  * codes are moved to it: exact, but for codes that become subnormal, which
- * round again.  What a page held before its first slot is written does not
+ * round again (a scale of 0 stands for zeros whatever the codes: those become
+ * zero codes).  What a page held before its first slot is written does not
  * matter (its scale included), so pages need no clearing when they are reused;
  * slots past the new tokens are not touched.  lens is not updated.  A page that
  * receives tokens must stand once in the tables (two writers of one page leave

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
     const float s_new = fmaxf(pow2_scale(fmaxf(tops.x, tops.y)), old);
     const float inv = s_new > 0.f ? 1.f / s_new : 0.f;  // exact
     if (threadIdx.x == 0) *scale = s_new;
-    if (old > 0.f && old < s_new) {  // the held codes move to the larger scale
+    if (s0 > 0 && old < s_new) {  // the held codes move to the larger scale (from 0: they stand for zeros)
         const float ratio = old * inv;
         uint32_t* held = reinterpret_cast<uint32_t*>(codes);
         for (int i = threadIdx.x; i < s0 * (D / 4); i += 128) {

@@ -1,0 +1,73 @@
+"""Values that the 8-bit cache meets at its edges, on a B200: pages blanked by their
+scale, elements that are not finite, rows of NaN in attention, and long walks of the
+tensor-memory tiles.
+
+Codes and scales are decisions of exact arithmetic and have to be equal; the
+attention's tolerance is that of test_cache8_gpu.
+"""
+
+import math
+
+import numpy as np
+import pytest
+
+import token_ref as ref
+from test_cache8_gpu import TYPES, check_attend, f64, filled_cache, ints, tables
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from io_aware_exact_30_b200 import attn  # noqa: E402
+
+
+def page_after(rows, held, old):
+    """(codes of the held slots, codes of the rows, scale) of one page and head after
+    rows (n, d) came behind the held codes: the definition, an element that is not
+    finite left out of the scale and stored as NaN."""
+    fine = np.isfinite(rows)
+    s = max(ref.page_scale(float(np.abs(np.where(fine, rows, 0)).max())), old if len(held) else 0.0)
+    new = np.where(fine, ref.e4m3_round(np.where(fine, rows, 0) / s) if s else 0.0, np.nan)
+    return (ref.e4m3_round(held * (old / s)) if s > old else held), new, s
+
+
+def append_and_compare(k, v, cache, page_id, fill):
+    """Appends k, v (1, Hkv, T, d) behind the first `fill` slots of a page; compares
+    codes (where the scale is 0 and stays 0, the values) and scales with page_after."""
+    before = [f64(x) for x in cache]
+    T = k.shape[2]
+    attn.cache_append(k, v, cache, ints([[page_id]]), ints([fill]))
+    assert attn.attn_last_device_status() == 0
+    for i, x in ((0, k), (1, v)):
+        codes, scale = f64(cache[i])[page_id], f64(cache[i + 2])[page_id]
+        for h in range(k.shape[1]):
+            held, new, s = page_after(f64(x)[0, h], before[i][page_id, h, :fill], before[i + 2][page_id, h])
+            assert scale[h] == s
+            assert np.array_equal(codes[h, :fill], held, equal_nan=True), cache._fields[i]
+            assert np.array_equal(codes[h, fill:fill + T], new, equal_nan=True), cache._fields[i]
+            assert np.array_equal(codes[h, fill + T:], before[i][page_id, h, fill + T:])
+
+
+@pytest.mark.parametrize("page,d,dtype,fill,T", [(16, 64, "bf16", 2, 1), (32, 128, "fp16", 31, 1),
+                                                 (64, 128, "bf16", 7, 40), (128, 64, "fp16", 100, 28)])
+def test_append_behind_tokens_of_a_zero_scale(page, d, dtype, fill, T):
+    """Tokens whose page has scale 0 stand for zeros, whatever their codes; they still
+    do when a new token brings the page a scale."""
+    cache = filled_cache(3, 2, page, d, 50)
+    cache.k_scale[1, 0] = 0.0
+    cache.v_scale[1, 1] = 0.0
+    g = torch.Generator().manual_seed(51)
+    k, v = (torch.randn(1, 2, T, d, generator=g).to(TYPES[dtype]).cuda() for _ in range(2))
+    append_and_compare(k, v, cache, 1, fill)
+    for codes, h in ((cache.k, 0), (cache.v, 1)):
+        assert (codes[1, h, :fill].float() == 0).all()
+
+
+def test_append_of_zeros_behind_tokens_of_a_zero_scale():
+    """The scale stays 0: the held tokens' values do too."""
+    cache = filled_cache(2, 1, 16, 64, 52)
+    cache.k_scale.zero_(), cache.v_scale.zero_()
+    x = torch.zeros(1, 1, 2, 64, device="cuda").bfloat16()
+    append_and_compare(x, x, cache, 0, 3)
+    x = x + 1
+    append_and_compare(x, x, cache, 0, 5)
+    assert (cache.k[0, 0, :5].float() == 0).all()
