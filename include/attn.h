@@ -259,9 +259,9 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * attn_cache_append: stores the first n_new[b] (NULL: all T) of the T new
  * tokens of k, v (B, Hkv, T, d) of each sequence b behind the lens[b] tokens it
  * holds.  The scale of each page and head the new tokens touch becomes the
- * least power of two s with |x| <= 448 s for all its new values, or stays if it
- * was larger and the page held tokens of this sequence before (slot 0 < fill);
- * codes are e4m3(x / s), nearest even.  When the scale of a page grows, the held
+ * least power of two s with |x| <= 448 s for all its new finite values, or stays
+ * if it was larger and the page held tokens of this sequence before (slot 0 <
+ * fill); codes are e4m3(x / s), nearest even, and NaN for an infinity or NaN.  When the scale of a page grows, the held
  * codes are moved to it: exact, but for codes that become subnormal, which
  * round again (a scale of 0 stands for zeros whatever the codes: those become
  * zero codes).  What a page held before its first slot is written does not

@@ -105,6 +105,30 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
     const float old = s0 > 0 ? *scale : 0.f;
     __syncthreads();
     top = __vmaxu2(__vmaxu2(warp_max[0], warp_max[1]), __vmaxu2(warp_max[2], warp_max[3]));
+    constexpr uint32_t kFinite = BF16 ? 0x7f7f7f7fu : 0x7bff7bffu;  // the type's largest, twice
+    if (__vmaxu2(top, kFinite) != kFinite) {
+        // an element that is not finite becomes a NaN code; the scale is that of the others
+        top = 0u;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int s = (static_cast<int>(threadIdx.x) + 128 * i) / PER_ROW;
+            if (s >= s0 && s < s1) {
+                uint32_t* w = &x[i].x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t bad = __vcmpgtu2(w[e] & 0x7fff7fffu, kFinite);
+                    w[e] |= bad & 0x7fff7fffu;
+                    top = __vmaxu2(top, w[e] & ~bad & 0x7fff7fffu);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
+        __syncthreads();  // every warp has read the first maxima
+        if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
+        __syncthreads();
+        top = __vmaxu2(__vmaxu2(warp_max[0], warp_max[1]), __vmaxu2(warp_max[2], warp_max[3]));
+    }
     const float2 tops = unpack2<BF16>(top);
     const float s_new = fmaxf(pow2_scale(fmaxf(tops.x, tops.y)), old);
     const float inv = s_new > 0.f ? 1.f / s_new : 0.f;  // exact

@@ -71,3 +71,39 @@ def test_append_of_zeros_behind_tokens_of_a_zero_scale():
     x = x + 1
     append_and_compare(x, x, cache, 0, 5)
     assert (cache.k[0, 0, :5].float() == 0).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("where", [(4,), (7,), (4, 7), tuple(range(64))])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fill", [0, 5])
+def test_append_of_elements_that_are_not_finite(bad, where, dtype, fill):
+    """They become NaN codes and cost the page's other elements nothing: neither those
+    of the same token, nor its neighbours, nor the tokens held before.  The largest
+    finite value stands in an even and in an odd feature."""
+    page, d = 32, 64
+    g = torch.Generator().manual_seed(53)
+    for top in (6, 11):
+        cache = filled_cache(2, 2, page, d, 54)
+        k, v = (torch.randn(1, 2, 6, d, generator=g) * 0.1 for _ in range(2))
+        k[0, 0, 3, top], v[0, 1, 0, top] = 30.0, -50.0
+        k[0, 0, 2, list(where)] = bad
+        v[0, 1, 5, list(where)] = bad
+        k, v = (x.to(TYPES[dtype]).cuda() for x in (k, v))
+        append_and_compare(k, v, cache, 1, fill)
+        assert torch.isnan(cache.k[1, 0, fill + 2].float()).sum() == len(where)
+
+
+def test_drafts_in_front_of_a_token_of_nan_read_on_after_it_is_taken_back():
+    """Five drafted tokens, the fourth NaN; with the length set back to the first three,
+    attention is exact over what they hold."""
+    page, d = 32, 128
+    cache = filled_cache(4, 2, page, d, 55)
+    g = torch.Generator().manual_seed(56)
+    k, v = (torch.randn(1, 2, 5, d, generator=g).bfloat16().cuda() for _ in range(2))
+    k[:, :, 3], v[:, :, 3] = math.nan, math.nan
+    table = ints([[2, 0, 3, 1]])
+    attn.cache_append(k, v, cache, table, ints([40]))
+    for Hq in (2, 24):
+        q = torch.randn(1, Hq, 3, d, generator=g).bfloat16().cuda()
+        check_attend(q, cache, table, [43])
