@@ -275,8 +275,11 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * the queries included; query t of its q_lens[b] (NULL: T) queries stands at
  * position lens[b] - q_lens[b] + t and sees, when causal, the keys up to its
  * own position, else all lens[b].  o (B, Hq, T, d) and lse (B, Hq, T) fp32 as
- * attn_fwd writes them; a query that sees no key gets O = 0 and lse = -inf;
- * rows t >= q_lens[b] are left as they were.  max_len: an upper bound of lens
+ * attn_fwd writes them; a query that sees no key gets O = 0 and lse = -inf, one
+ * that holds a NaN, or sees a NaN in a key, NaN in both; rows t >= q_lens[b] are
+ * left as they were.  A NaN in a value of the lens[b] tokens may reach that feature
+ * of every query of the sequence, those in front of the token included (its weight
+ * there is 0, but 0 NaN is NaN); slots past lens[b] may hold anything.  max_len: an upper bound of lens
  * that sizes the split of long sequences over the device (a larger one costs
  * time, a sequence longer than it is still attended to in full).  Sums are fp32
  * and divided at the end: o is finite for values up to 2^64.  workspace:

@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) cache_attend_kernel(cons
     const int rr = mt * ROWS + r;
     const size_t row = (static_cast<size_t>(b) * p.Hq + hk * G + rr % G) * p.T + rr / G;
     // both o and the sums carry P's storage factor: it leaves with the division,
-    // and is taken out of the sum for the logarithm
-    const float inv = whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f;
+    // and is taken out of the sum for the logarithm.  A sum is 0 only where no key was
+    // seen; a NaN must not be taken for that.
+    const float inv = whole ? (ll != 0.f ? 1.f / ll : 0.f) : 1.f;
 #pragma unroll
     for (int c = c0 * 4; c < D; c += PER * 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) cache_attend_kernel(cons
     }
     if (c0 == 0) {
         if (whole)
-            p.lse[row] = ll > 0.f ? (mm + (log2f(ll) - kUp)) * 0.6931471805599453f : -INFINITY;
+            p.lse[row] = ll != 0.f ? (mm + (log2f(ll) - kUp)) * 0.6931471805599453f : -INFINITY;
         else
             p.part_ml[row * p.nsplit + split] = make_float2(mm - kUp, ll);
     }
@@ -697,9 +698,9 @@ __global__ void __launch_bounds__(256) cache_attend_join_kernel(const AttendPara
         v.x += so[w][2 * threadIdx.x], v.y += so[w][2 * threadIdx.x + 1];
         ll += sl[w];
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = ll != 0.f ? 1.f / ll : 0.f;
     reinterpret_cast<uint32_t*>(p.o)[row * (D / 2) + threadIdx.x] = pack2<BF16>(v.x * inv, v.y * inv);
-    if (threadIdx.x == 0) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    if (threadIdx.x == 0) p.lse[row] = ll != 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Rows of a CTA: 8, or 16 when there are more than 8 (the codes' conversion is

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
             const float mm = fmaxf(a.x, d.x);
             const float fa = a.x == -INFINITY ? 0.f : ex2(a.x - mm), fd = d.x == -INFINITY ? 0.f : ex2(d.x - mm);
             const float ll = fa * a.y + fd * d.y;
-            const float inv = whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f;
+            const float inv = whole ? (ll != 0.f ? 1.f / ll : 0.f) : 1.f;
             const size_t at = (static_cast<size_t>(b) * p.Hq + hk * G + qq % G) * p.T + qq / G;
 #pragma unroll 4
             for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 4) {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(640, 1) cache_attend_tile_kernel(const AttendP
             }
             if (part == 0) {
                 if (whole)
-                    p.lse[at] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                    p.lse[at] = ll != 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
                 else
                     p.part_ml[at * p.nsplit + split] = make_float2(mm, ll);
             }

@@ -107,3 +107,38 @@ def test_drafts_in_front_of_a_token_of_nan_read_on_after_it_is_taken_back():
     for Hq in (2, 24):
         q = torch.randn(1, Hq, 3, d, generator=g).bfloat16().cuda()
         check_attend(q, cache, table, [43])
+
+
+@pytest.mark.parametrize("Hq,T,lens", [(2, 2, [30, 600]),         # fragments of 8 rows, one split and several
+                                       (12, 1, [30, 600]),        # of 16
+                                       (40, 1, [30, 2000]),       # tiles
+                                       (1, 1, [1, 9000])])
+def test_attention_of_a_query_of_nan_is_nan(Hq, T, lens):
+    """O and the log-sum-exp of a row that holds a NaN or sees a NaN key are NaN: a
+    caller who joins parts by their log-sum-exp must not take it for a row that sees
+    nothing (-inf).  The other rows stay right."""
+    page, d, B = 16, 128, 2
+    P, table = tables(B, -(-max(lens) // page), 57)
+    cache = filled_cache(P, 1, page, d, 58)
+    q = torch.randn(B, Hq, T, d, generator=torch.Generator().manual_seed(59)).bfloat16().cuda()
+    first = [x[0].clone() for x in attn.cache_attend(q, cache, table, ints(lens))]
+    bad = q.clone()
+    bad[1, 0, T - 1, 17] = math.nan
+    o, lse = attn.cache_attend(bad, cache, table, ints(lens))
+    assert torch.isnan(o[1, 0, T - 1]).all() and torch.isnan(lse[1, 0, T - 1])
+    # (which row moves the reference of a warp's rows may change their last bits)
+    want, lse_w, weight, mag = ref.attend(f64(q), *(f64(x) for x in cache), table.cpu().numpy(), lens, [T] * B,
+                                          True, 1 / math.sqrt(d))
+    delta = 2.0 ** -16 * mag
+    tol = torch.finfo(q.dtype).eps / 2 * np.abs(want) + (2.0 ** -11 + 2 * delta[..., None]) * weight
+    same = np.ones((B, Hq, T), bool)
+    same[1, 0, T - 1] = False
+    assert np.all((np.abs(f64(o) - want) <= tol)[same])
+    with np.errstate(invalid="ignore"):
+        assert np.all(((np.abs(f64(lse) - lse_w) <= delta + 2.0 ** -20) | (f64(lse) == lse_w))[same])
+    # a key of NaN in the first page of the longer sequence, seen by all its rows
+    cache.k.view(torch.uint8)[table[1, 0].long(), 0, 0, 5] = 0x7F
+    o, lse = attn.cache_attend(q, cache, table, ints(lens))
+    assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.equal(o[0], first[0]) and torch.equal(lse[0], first[1])
+    assert attn.attn_last_device_status() == 0
