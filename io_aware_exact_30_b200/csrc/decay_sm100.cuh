@@ -57,6 +57,14 @@ __device__ __forceinline__ float decay_log(const float* log_decay, int h) {
     return x < -1e4f ? -1e4f : x;  // NaN stays
 }
 
+// The power of two that brings values of largest magnitude `top` to 2^14 .. 2^15, where
+// fp16 holds all that is above 2^-29 of it as normal numbers; its inverse is a normal
+// number too.
+__device__ __forceinline__ float fp16_up(float top) {
+    const int e = 268 - static_cast<int>(__float_as_uint(top) >> 23);
+    return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : (e > 253 ? 253 : e)) << 23);
+}
+
 constexpr int kDecayChunk = 128;
 
 // Tokens of segment `seg` of a sequence of n: chunks [c0, c1).
@@ -81,24 +89,33 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // 16-bit type (one bf16 piece of it would be off by up to 2^-8, two by 2^-16): it
 // goes to the tensor cores as two (fp16, 22 bits) or three (bf16, 24 bits) 16-bit
 // pieces, side by side in the N extent of one product with Y, and the pieces' sums
-// are added in fp32.  P, the copy of S that X meets and the result are rounded to
+// are added in fp32.  fp16 has no range for that by itself (terms of 1e-5 would be off by
+// 1e-5 of themselves, those of a loss scaled up past 65504 be lost): Z is brought to the
+// top of it by a power of two for each chunk and 8 features, of their largest finite
+// element, which leaves with the sums in fp32, as the scale of a backward pass does.  A term
+// keeps its 22 bits down to 2^-29 of the largest, and is off by 2^-51 of that below.  P,
+// the copy of S that X meets and the result are rounded to
 // the 16-bit type, half a step each: they only reach the 16-bit result.
 //
-// What bounds it: shared memory and the hand-overs.  At D = 128 a chunk's products
-// take about 2150 cycles of the tensor pipe, and the operands they read, the loads,
-// Zh, the state's copy and the staged result about 3100 cycles of shared-memory
-// bandwidth; the roles' chain makes 4700 of it (2.4 us a chunk).  HBM would allow 1.3 us.
+// What bounds it: the chain of the roles from one chunk to the next, 4700 cycles of it at
+// D = 128 (2.4 us a chunk), in which a role waits for what another hands over.  The
+// products take about 2150 cycles of the tensor pipe; the operands they read, the loads,
+// Zh, the state's copy and the staged result about 3100 cycles of shared-memory bandwidth.
+// HBM would allow 1.3 us.
 // Measured (one B200, device time): 4 x 16 heads of 4096 tokens, d = 128, bf16: 85 us
 // (269 MB and states: 3.2 TB/s), the gradients 236 us; 12 heads of 23400 tokens,
 // d = 64, fp16, in 12 segments: 64 us.  The same kernel without Zh, P and stores: 57 us.
 //
 // Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
-// products, warp 2 stores (TMA), 3 fills rows past the end; 16 warps make P and the output (thread = token;
-// each 32 keys of P and 16 features); 4 hold the state (thread = feature of y); 8 make
-// Zh (thread = token, 32 features each).  Every role's work lies on the chain from
-// one chunk to the next (Zh is written when its last reader is done), so it is spread
-// over as many warps as the registers carry (8 row warps and 16 for Zh instead: 87.6
-// against 85.6 us for the large-head prompt).  Registers are dealt out between the warpgroups (setmaxnreg).
+// products, warp 2 stores (TMA), 3 fills rows past the end; 16 warps make P and the
+// output (thread = token; each 32 keys of P and 16 features); 4 hold the state (thread =
+// feature of y); 8 make Zh (bf16: thread = token, 32 features each; fp16: 8 features of
+// all tokens, whose largest a warp then knows by itself; 12 heads of 23400 tokens take 64.8
+// us so, 67.5 with bf16's way and a barrier between the warps, 61.6 without the powers of
+// two).  Every role's work lies on the chain (Zh is written when its last reader is done),
+// so it is spread over as many warps as the registers carry (8 row warps and 16 for Zh
+// instead: 87.6 against 85.6 us for the large-head prompt).  Registers are dealt out
+// between the warpgroups (setmaxnreg).
 // Issue order: A_0, then per chunk Y^T Zh, X S, A of the next chunk, P Z: while the
 // row warps read X S and hand over P, the next A runs, and the next P is made during
 // P Z and Y^T Zh.  Every product has a completion barrier for either stage, on which
@@ -109,8 +126,7 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 template <int D, bool BF16>
 struct DecayCfg {
     static constexpr int NP = BF16 ? 3 : 2;             // pieces of Zh
-    // fp16's second piece is stored times 2^11, the first one's size, so that small
-    // values keep their bits (unscaled, terms of 1e-5 would be off by 1e-3)
+    // fp16's second piece is stored times 2^11, the first one's size
     static constexpr float PIECE_UP = BF16 ? 1.f : 2048.f;
     static constexpr uint32_t XB = D * 256u;            // X of a chunk
     static constexpr uint32_t YB = 32768u;              // Y; at D = 64 its upper half stays zero
@@ -132,7 +148,10 @@ struct DecayCfg {
     static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_AF = 6, B_KVF = 8, B_QSD = 10, B_OD = 12,
                          B_PF = 14, B_ZH = 15, B_KVE = 16, B_SSF = 17, B_OE = 18, B_DR = 19, B_OR = 20,
                          B_OW = 22, NBAR = 24;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
+    // fp16: what takes Z's power of two out of the sums of each 8 features, of four chunks
+    // (the state warps may still read a chunk's when the Zh warps are two on)
+    static constexpr uint32_t OFF_ZD = OFF_BAR + NBAR * 8;
+    static constexpr uint32_t OFF_MISC = OFF_ZD + (BF16 ? 0 : 4 * 8 * 4);
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;
     static constexpr uint32_t COL_KV = 256, COL_O = 448;  // tensor memory: A at 0 and 128
     static constexpr int NROW = 512, NSTATE = 128, NZH = 256, NTHREADS = 1024;
@@ -175,6 +194,7 @@ __global__ void __launch_bounds__(1024, 1)
     volatile uint32_t* abort_flag = tmem_slot + 1;
     float* pw = reinterpret_cast<float*>(gbase + C::OFF_PW) + 32;
     const double ld = decay_log(p.log_decay, bh % p.H);
+    float* zd = reinterpret_cast<float*>(gbase + C::OFF_ZD);
     // of step i: Y (what 0), X (1), Z (2)
     auto load = [&](int i, int what) {
         const int s = i & 1, row = chunk(i) * kDecayChunk;
@@ -536,6 +556,8 @@ __global__ void __launch_bounds__(1024, 1)
                 uint32_t v[NP][16];
 #pragma unroll
                 for (int k = 0; k < NP; ++k) tmem_ld16(lane_addr + C::COL_KV + 64u * k + 16u * cc, v[k]);
+                const float2 down = BF16 ? make_float2(1.f, 1.f)
+                                         : *reinterpret_cast<const float2*>(zd + (i & 3) * 8 + 2 * cc);
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < NP; ++k)
@@ -548,6 +570,7 @@ __global__ void __launch_bounds__(1024, 1)
                     for (int k = NP - 2; k >= 0; --k)  // the small pieces first
                         sum = fma2(sum, f2(1.f / C::PIECE_UP, 1.f / C::PIECE_UP),
                                    f2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])));
+                    if (!BF16) sum = mul2(sum, e < 4 ? f2(down.x, down.x) : f2(down.y, down.y));
                     uint64_t& x = st[8 * cc + e];
                     x = fma2(g, x, fma2(g2, x, sum));
                 }
@@ -573,58 +596,97 @@ __global__ void __launch_bounds__(1024, 1)
     } else {
         // -------------------------------------------------------------- Zh
         regs_down<C::R_ZH>();
-        const int a = (warp & 3) * 32 + lane;  // token
-        const int j0 = (warp - 24) >> 2 << 2;  // features 8 j0 ..
-        const float zscale = rev ? p.scale : 1.f;
+        // four 16-byte pieces (8 features of a token) a thread: bf16, four of one token;
+        // fp16, the same features of four tokens, so that a warp by itself knows the
+        // largest element of its 8 features
+        auto token = [&](int t) { return BF16 ? (warp & 3) * 32 + lane : 32 * t + lane; };
+        auto piece = [&](int t) { return BF16 ? ((warp - 24) >> 2 << 2) + t : warp - 24; };
+        auto at = [&](int t) { return static_cast<uint32_t>(token(t) * 128 + ((piece(t) ^ (token(t) & 7)) << 4)); };
         for (int i = 0; i < nch; ++i) {
             const int s = i & 1, n = tokens(i);
-            // Z landed; the previous product has read Zh
-            bool ok = wait_bounded(DBAR(C::B_ZF + s), (i >> 1) & 1, abort_flag) &&
-                      (i == 0 || wait_bounded(DBAR(C::B_KVF + (s ^ 1)), ((i - 1) >> 1) & 1, abort_flag));
+            uint8_t* zt = gbase + s * C::STAGE + C::XB + C::YB;
+            uint8_t* ht = gbase + C::OFF_ZH;
+            // Z landed
+            bool ok = wait_bounded(DBAR(C::B_ZF + s), (i >> 1) & 1, abort_flag);
+            uint4 in[4];
+            float up = rev ? p.scale : 1.f;
+            auto load_z = [&]() {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    in[t] = token(t) < n ? *reinterpret_cast<const uint4*>(zt + at(t)) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            if constexpr (!BF16) {
+                if (!__all_sync(0xffffffffu, ok)) break;
+                load_z();
+                __half2 top2 = __float2half2_rn(0.f);  // (its maximum passes over NaN)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t z[4] = {in[t].x, in[t].y, in[t].z, in[t].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&z[e])));
+                }
+                const float2 tf = __half22float2(top2);
+                uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(tf.x, tf.y)));
+                if (top >= 0x7f800000u) {  // an infinity: the largest finite one
+                    float most = 0.f;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t z[4] = {in[t].x, in[t].y, in[t].z, in[t].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = unpack2<false>(z[e]);
+                            most = fmaxf(most, isfinite(f.x) ? fabsf(f.x) : 0.f);
+                            most = fmaxf(most, isfinite(f.y) ? fabsf(f.y) : 0.f);
+                        }
+                    }
+                    top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+                }
+                const float down = up;
+                up = fp16_up(__uint_as_float(top));
+                if (lane == 0) zd[(i & 3) * 8 + piece(0)] = down / up;
+            }
+            // the previous product has read Zh
+            ok = ok && (i == 0 || wait_bounded(DBAR(C::B_KVF + (s ^ 1)), ((i - 1) >> 1) & 1, abort_flag));
             if (n < kDecayChunk)  // Y is cleared below
                 ok = ok && wait_bounded(DBAR(C::B_YF + s), (i >> 1) & 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t* zrow = gbase + s * C::STAGE + C::XB + C::YB + a * 128;
-            uint8_t* hrow = gbase + C::OFF_ZH + a * 128;
-            if (a < n) {
-                const float w = (rev ? pw[a + 1] : pw[n - 1 - a]) * zscale;
-                const uint64_t w2 = f2(w, w), minus = f2(-1.f, -1.f);
+            if constexpr (BF16) load_z();
+            const uint64_t minus = f2(-1.f, -1.f);
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    const uint32_t at = ((j0 + jj) ^ (a & 7)) << 4;
-                    const uint4 in = *reinterpret_cast<const uint4*>(zrow + at);
-                    const uint32_t z[4] = {in.x, in.y, in.z, in.w};
-                    uint32_t out[NP][4];
+            for (int t = 0; t < 4; ++t) {
+                // (past the end in is zero, whatever its weight)
+                const float w = up * (rev ? pw[token(t) + 1] : pw[max(n - 1 - token(t), 0)]);
+                const uint64_t w2 = f2(w, w);
+                const uint32_t z[4] = {in[t].x, in[t].y, in[t].z, in[t].w};
+                uint32_t out[NP][4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 zf = unpack2<BF16>(z[e]);
-                        uint64_t f = mul2(f2(zf.x, zf.y), w2);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 zf = unpack2<BF16>(z[e]);
+                    uint64_t f = mul2(f2(zf.x, zf.y), w2);
 #pragma unroll
-                        for (int k = 0; k < NP; ++k) {
-                            const float2 x = unf2(f);
-                            out[k][e] = pack2<BF16>(x.x, x.y);
-                            const float2 h = unpack2<BF16>(out[k][e]);
-                            f = fma2(f2(h.x, h.y), minus, f);
-                            if (!BF16) f = mul2(f, f2(C::PIECE_UP, C::PIECE_UP));
-                        }
+                    for (int k = 0; k < NP; ++k) {
+                        const float2 x = unf2(f);
+                        out[k][e] = pack2<BF16>(x.x, x.y);
+                        const float2 h = unpack2<BF16>(out[k][e]);
+                        f = fma2(f2(h.x, h.y), minus, f);
+                        if (!BF16) f = mul2(f, f2(C::PIECE_UP, C::PIECE_UP));
                     }
-#pragma unroll
-                    for (int k = 0; k < NP; ++k)
-                        *reinterpret_cast<uint4*>(hrow + k * C::ZB + at) =
-                            make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
                 }
-            } else {
-                // a token past the end: it may hold anything, NaN included, in y and z
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    *reinterpret_cast<uint4*>(ht + k * C::ZB + at(t)) =
+                        make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+            }
+            if (n < kDecayChunk) {
+                // tokens past the end may hold anything, NaN included, in y and z
                 const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int j = j0; j < j0 + 4; ++j) {
-                    *reinterpret_cast<uint4*>(zrow + j * 16) = none;
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4*>(hrow + k * C::ZB + j * 16) = none;
+                for (int t = 0; t < 4; ++t) {
+                    if (token(t) < n) continue;
+                    *reinterpret_cast<uint4*>(zt + at(t)) = none;
 #pragma unroll
                     for (int k = 0; k < HALVES; ++k)
-                        *reinterpret_cast<uint4*>(gbase + s * C::STAGE + C::XB + k * 16384u + a * 128 + j * 16) =
-                            none;
+                        *reinterpret_cast<uint4*>(zt - C::YB + k * 16384u + at(t)) = none;
                 }
             }
             fence_proxy_async_smem();

@@ -140,6 +140,26 @@ def check_all(xs, s0, ds, ld, dtype, lens=None, state_tol=STATE_TOL, heads=slice
     assert rel(got[3][:, heads], want[3]) <= state_tol, ("dstate", rel(got[3][:, heads], want[3]))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-5, 1e-6])
+def test_states_of_fp16_values_of_every_size(d, size):
+    """States are fp32: terms of values far below fp16's smallest normal number (6e-5)
+    keep their bits on the way through 16-bit pieces."""
+    N = 333
+    (q, k, v, do), _ = scaled(71, N, d, "fp16", (1, 1, size, size))
+    ld = torch.tensor(SLOW, device="cuda")
+    zero = torch.zeros(1, 3, d, d, device="cuda")
+    _, s1 = attn.decay_forward(q, k, v, ld)
+    ds = attn.decay_backward(q, k, v, ld, do)[3]
+    _, want, grads = gradients(q, k, v, ld, do, zero, zero, ints([N]).long(), 1 / math.sqrt(d))
+    assert rel(s1, want) <= STATE_TOL and rel(ds, grads[3]) <= STATE_TOL
+    # few heads and a long sequence: the segments' own sums
+    (q, k, v, do), _ = scaled(72, 2000, d, "fp16", (size, size, 1, 1))
+    ds = attn.decay_backward(q, k, v, ld, do)[3]
+    _, want, grads = gradients(q, k, v, ld, do, zero, zero, ints([2000]).long(), 1 / math.sqrt(d))
+    assert rel(attn.decay_forward(q, k, v, ld)[1], want) <= STATE_TOL and rel(ds, grads[3]) <= STATE_TOL
+
+
 # standard deviations of q, k, v and dout, and of the states; every result is within fp16's
 # normal range, what is rounded to 16 bits on the way to it would not be
 SIZES = {
