@@ -342,10 +342,12 @@ int attn_cache_attend(const void* q, const unsigned char* k8, const unsigned cha
  * attn_decay_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0); its
  * contents on entry do not matter.  Every sum is made in a fixed order: results
  * repeat bit for bit.  States are fp32 throughout (errors of about 2^-22, of inputs of
- * any size); in the chunked forms the 16-bit results see a state (times scale,
- * forwards) and the in-chunk weights scale q.k g^distance rounded to their type: in
- * fp16 those must stay within 65504, and lose relative precision below 2^-14 (bf16 has
- * fp32's range).  A NaN in log_decay makes its head NaN.  Errors as attn_fwd.
+ * any size); in the chunked forms the 16-bit results see a state and the in-chunk
+ * weights scale q.k g^distance rounded to their type's precision, in fp32's range (fp16
+ * under powers of two for each 128 tokens: a weight to 2^-11, or to 2^-39 of d scale
+ * max|q| max|k| if that is more).  A NaN in log_decay makes its head NaN; an
+ * infinity or NaN in a row spoils the results that it reaches, and may spoil its
+ * feature in the rows of its 128 tokens that stand in front of it.  Errors as attn_fwd.
  */
 size_t attn_decay_workspace_bytes(int B, int H, int N, int d, int backward);
 

@@ -58,12 +58,15 @@ __device__ __forceinline__ float decay_log(const float* log_decay, int h) {
 }
 
 // The power of two that brings values of largest magnitude `top` to 2^14 .. 2^15, where
-// fp16 holds all that is above 2^-29 of it as normal numbers; its inverse is a normal
-// number too.
+// fp16 holds all that is above 2^-29 of it as normal numbers (1 for 0 and NaN); its
+// inverse is a normal number too.
 __device__ __forceinline__ float fp16_up(float top) {
-    const int e = 268 - static_cast<int>(__float_as_uint(top) >> 23);
+    const int e = top > 0.f ? 268 - static_cast<int>(__float_as_uint(top) >> 23) : 127;
     return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : (e > 253 ? 253 : e)) << 23);
 }
+
+// The inverse of a power of two that fp16_up gives.
+__device__ __forceinline__ float fp16_down(float up) { return __uint_as_float((254u << 23) - __float_as_uint(up)); }
 
 constexpr int kDecayChunk = 128;
 
@@ -89,13 +92,23 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // 16-bit type (one bf16 piece of it would be off by up to 2^-8, two by 2^-16): it
 // goes to the tensor cores as two (fp16, 22 bits) or three (bf16, 24 bits) 16-bit
 // pieces, side by side in the N extent of one product with Y, and the pieces' sums
-// are added in fp32.  fp16 has no range for that by itself (terms of 1e-5 would be off by
-// 1e-5 of themselves, those of a loss scaled up past 65504 be lost): Z is brought to the
-// top of it by a power of two for each chunk and 8 features, of their largest finite
-// element, which leaves with the sums in fp32, as the scale of a backward pass does.  A term
-// keeps its 22 bits down to 2^-29 of the largest, and is off by 2^-51 of that below.  P,
-// the copy of S that X meets and the result are rounded to
-// the 16-bit type, half a step each: they only reach the 16-bit result.
+// are added in fp32.  P, the copy of S that X meets and the result are rounded to the
+// 16-bit type, half a step each: they only reach the 16-bit result.
+//
+// fp16 has no range for that by itself (terms of 1e-5 would be off by 1e-5 of themselves,
+// weights of 1e-5 by 4e-3, a state or a weight past 65504 be lost).  What goes to the tensor
+// cores is brought to the top of its range by exact powers of two:
+//   Zh  for each chunk and 8 features, by their largest finite element; it leaves with the
+//       sums in fp32, as the scale of a backward pass does.  A term keeps its 22 bits down
+//       to 2^-17 of the largest, and is off by 2^-39 of that below
+//   P   for each 16 rows, by the bound D max|X| max|Y| of their A, whose products the tensor
+//       cores add in fp32, 2^-24 of it apart: a weight keeps its 11 bits down to 2^-28 of
+//       the bound, and is off by 2^-39 of that below
+//   S   for each chunk, by a bound that starts with the largest element and grows by 128
+//       max|Y| max|Z| a chunk, as the state's own rounding errors do; likewise
+// The maxima of X and Y are surveyed by the Zh warps, before Z lands.  (Exact maxima of P,
+// over which the four warps of the same rows meet: 12 heads of 23400 tokens 84 us; the survey
+// by a warp of its own 82, by the state warps 94; as it is 73; without P's and S's powers 65.)
 //
 // What bounds it: the chain of the roles from one chunk to the next, 4700 cycles of it at
 // D = 128 (2.4 us a chunk), in which a role waits for what another hands over.  The
@@ -110,9 +123,9 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 // products, warp 2 stores (TMA), 3 fills rows past the end; 16 warps make P and the
 // output (thread = token; each 32 keys of P and 16 features); 4 hold the state (thread =
 // feature of y); 8 make Zh (bf16: thread = token, 32 features each; fp16: 8 features of
-// all tokens, whose largest a warp then knows by itself; 12 heads of 23400 tokens take 64.8
-// us so, 67.5 with bf16's way and a barrier between the warps, 61.6 without the powers of
-// two).  Every role's work lies on the chain (Zh is written when its last reader is done),
+// all tokens, whose largest a warp then knows by itself; without P's and S's powers 12 heads
+// of 23400 tokens take 64.8 us so, 67.5 with bf16's way and a barrier between the warps, 61.6
+// without any).  Every role's work lies on the chain (Zh is written when its last reader is done),
 // so it is spread over as many warps as the registers carry (8 row warps and 16 for Zh
 // instead: 87.6 against 85.6 us for the large-head prompt).  Registers are dealt out
 // between the warpgroups (setmaxnreg).
@@ -126,8 +139,6 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 template <int D, bool BF16>
 struct DecayCfg {
     static constexpr int NP = BF16 ? 3 : 2;             // pieces of Zh
-    // fp16's second piece is stored times 2^11, the first one's size
-    static constexpr float PIECE_UP = BF16 ? 1.f : 2048.f;
     static constexpr uint32_t XB = D * 256u;            // X of a chunk
     static constexpr uint32_t YB = 32768u;              // Y; at D = 64 its upper half stays zero
     static constexpr uint32_t ZB = 16384u;              // 64 features of Z
@@ -147,17 +158,22 @@ struct DecayCfg {
     // two each of the loads and the products (by step parity), one of the rest
     static constexpr int B_XF = 0, B_YF = 2, B_ZF = 4, B_AF = 6, B_KVF = 8, B_QSD = 10, B_OD = 12,
                          B_PF = 14, B_ZH = 15, B_KVE = 16, B_SSF = 17, B_OE = 18, B_DR = 19, B_OR = 20,
-                         B_OW = 22, NBAR = 24;
+                         B_OW = 22, B_SV = 24, B_SM = 26, NBAR = BF16 ? 24 : 27;
     // fp16: what takes Z's power of two out of the sums of each 8 features, of four chunks
     // (the state warps may still read a chunk's when the Zh warps are two on)
-    static constexpr uint32_t OFF_ZD = OFF_BAR + NBAR * 8;
-    static constexpr uint32_t OFF_MISC = OFF_ZD + (BF16 ? 0 : 4 * 8 * 4);
+    static constexpr uint32_t OFF_ZD = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
+    // the largest |X| of each 16 tokens and the largest |Y|, of four steps; what takes the
+    // state copy's power out, of two; the largest |S| that each state warp begins with
+    static constexpr uint32_t OFF_SX = OFF_ZD + 4 * 8 * 4, OFF_SY = OFF_SX + 4 * 8 * 4, OFF_SM = OFF_SY + 4 * 4,
+                              OFF_SD = OFF_SM + 4 * 4;
+    static constexpr uint32_t OFF_MISC = BF16 ? OFF_ZD : OFF_SD + 2 * 4;
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;
     static constexpr uint32_t COL_KV = 256, COL_O = 448;  // tensor memory: A at 0 and 128
     static constexpr int NROW = 512, NSTATE = 128, NZH = 256, NTHREADS = 1024;
     // registers of a thread by role; the launch gives each of the eight warpgroups 64
-    static constexpr int R_ISSUE = 32, R_ROW = 56, R_STATE = 144, R_ZH = 56;
+    static constexpr int R_ISSUE = BF16 ? 32 : 40, R_ROW = 56, R_STATE = BF16 ? 144 : 136, R_ZH = 56;
     static_assert(R_ISSUE + 4 * R_ROW + R_STATE + 2 * R_ZH <= 8 * 64, "more registers than the launch has");
+    static_assert(R_ISSUE <= 64 && R_ROW <= 64 && R_ZH <= 64 && R_STATE >= 64, "a share on the wrong side of the launch's");
     static_assert(SMEM_BYTES <= 232448u, "dynamic shared memory above the sm_100 per-block limit");
 };
 
@@ -195,6 +211,9 @@ __global__ void __launch_bounds__(1024, 1)
     float* pw = reinterpret_cast<float*>(gbase + C::OFF_PW) + 32;
     const double ld = decay_log(p.log_decay, bh % p.H);
     float* zd = reinterpret_cast<float*>(gbase + C::OFF_ZD);
+    float* sd = reinterpret_cast<float*>(gbase + C::OFF_SD);
+    float* sx = reinterpret_cast<float*>(gbase + C::OFF_SX);
+    float* sy = reinterpret_cast<float*>(gbase + C::OFF_SY);
     // of step i: Y (what 0), X (1), Z (2)
     auto load = [&](int i, int what) {
         const int s = i & 1, row = chunk(i) * kDecayChunk;
@@ -212,11 +231,14 @@ __global__ void __launch_bounds__(1024, 1)
     };
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
-            const int rows = i == C::B_PF || i == C::B_OE || i >= C::B_OW;
+            const int rows = i == C::B_PF || i == C::B_OE || i == C::B_OW || i == C::B_OW + 1;
             const int state = i == C::B_KVE || i == C::B_SSF;
-            mbar_init(DBAR(i), rows ? C::NROW : (state ? C::NSTATE : (i == C::B_ZH ? C::NZH : 1)));
+            mbar_init(DBAR(i), rows ? C::NROW
+                                    : (state ? C::NSTATE : (i == C::B_ZH ? C::NZH : (i == C::B_SM ? 4 : (i >= C::B_SV ? 8 : 1)))));
         }
         *abort_flag = 0u;
+        if (!BF16)
+            for (int i = 0; i < 4; ++i) sy[i] = 0.f;
         fence_mbar_init();
         // both stages are empty: their loads run while the tables are made
         for (int i = 0; i < 2 && i < nch; ++i)
@@ -292,6 +314,7 @@ __global__ void __launch_bounds__(1024, 1)
                 if (!wait3(DBAR(C::B_XF + s), (i >> 1) & 1, true, DBAR(C::B_YF + s), (i >> 1) & 1, true,
                            DBAR(C::B_OD + s), ((i >> 1) - 1) & 1, i >= 2, abort_flag))
                     return false;
+                if (!BF16 && !wait_bounded(DBAR(C::B_SV + s), (i >> 1) & 1, abort_flag)) return false;
                 if (tokens(i) < kDecayChunk && !wait_bounded(DBAR(C::B_ZH), i & 1, abort_flag)) return false;
                 tc_fence_after();
                 const uint64_t x = dx + s * ST16, y = x + (C::XB >> 4);
@@ -382,7 +405,9 @@ __global__ void __launch_bounds__(1024, 1)
         const int wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float* near = rev ? pw : pw + 132;
-        const bool steep = pw[31] < 0x1p-100f;  // L^-31 out of range
+        // L^-31 out of range (fp16: with P's power of two times scale, 2^63 at most, since no
+        // fp16 number but 0 is below 2^-24)
+        const bool steep = pw[31] < (BF16 ? 0x1p-100f : 0x1p-60f);
         uint32_t o16[8] = {};  // the output of a step, until it is staged
         auto stage = [&](int i) -> bool {
             const int b = i & 1, n = tokens(i);
@@ -413,6 +438,12 @@ __global__ void __launch_bounds__(1024, 1)
         for (int i = 0; !STATE && i < nch; ++i) {
             const int b = i & 1, n = tokens(i);
             if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_AF + b), (i >> 1) & 1, abort_flag)))) break;
+            float pscale = p.scale, pup = 1.f;
+            if constexpr (!BF16) {
+                // what bounds the row's A
+                pup = fp16_up(sx[(i & 3) * 8 + (r >> 4)] * sy[i & 3] * (D * p.scale));
+                pscale *= pup;
+            }
             tc_fence_after();
             {
                 const uint32_t col = lane_addr + 128u * b + 32u * cb;
@@ -429,15 +460,15 @@ __global__ void __launch_bounds__(1024, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const int gap = rev ? e - lane : lane - e;  // zeros in front of L^0
-                            const float x = __uint_as_float(v[e]) * (pw[gap] * p.scale);
+                            const float x = __uint_as_float(v[e]) * (pw[gap] * pscale);
                             v[e] = gap >= 0 ? __float_as_uint(x) : 0u;
                         }
                     } else {
                         // L^(distance) as L^(from the row to the block's near end) times
                         // L^(from there to the key): neither above 1 behind the row, and in
                         // the row's own block the first at most L^-31
-                        const float u = cb == wq ? p.scale / pw[rev ? lane : 31 - lane]
-                                                 : p.scale * (rev ? pw[cb * 32 - r] : pw[r - cb * 32 - 31]);
+                        const float u = cb == wq ? pscale / pw[rev ? lane : 31 - lane]
+                                                 : pscale * (rev ? pw[cb * 32 - r] : pw[r - cb * 32 - 31]);
                         const uint64_t u2 = f2(u, u);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -471,6 +502,8 @@ __global__ void __launch_bounds__(1024, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) reg_fence(ox[e]);
+            float w = r < n ? (rev ? pw[n - 1 - r] : pw[r + 1]) : 0.f, down = 1.f;
+            if (!BF16) w *= sd[b], down = fp16_down(pup);
             tc_fence_before();
             mbar_arrive(DBAR(C::B_PF));
             // in a buffer of its own the previous step's output is staged during P Z
@@ -484,11 +517,18 @@ __global__ void __launch_bounds__(1024, 1)
             for (int e = 0; e < 16; ++e) reg_fence(v[e]);
             tc_fence_before();
             mbar_arrive(DBAR(C::B_OE));
-            const float w = r < n ? (rev ? pw[n - 1 - r] : pw[r + 1]) : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
-                                     fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (BF16) {
+                    o16[e] = pack2<BF16>(fmaf(w, __uint_as_float(ox[2 * e]), __uint_as_float(v[2 * e])),
+                                         fmaf(w, __uint_as_float(ox[2 * e + 1]), __uint_as_float(v[2 * e + 1])));
+                } else {
+                    const float2 f = unf2(fma2(
+                        f2(w, w), f2(__uint_as_float(ox[2 * e]), __uint_as_float(ox[2 * e + 1])),
+                        mul2(f2(down, down), f2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])))));
+                    o16[e] = pack2<BF16>(f.x, f.y);
+                }
+            }
             if (!C::OWN_O && !(ok = stage(i))) break;
         }
         if (C::OWN_O && !STATE && ok && nch > 0) stage(nch - 1);
@@ -499,7 +539,9 @@ __global__ void __launch_bounds__(1024, 1)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const size_t mat = static_cast<size_t>(bh) * D * D;
         const size_t seg_mat = (static_cast<size_t>(pi) * p.nseg + seg) * p.B * p.H * D * D + mat;
-        const float copy = rev ? 1.f : p.scale;
+        float copy = rev ? 1.f : p.scale;
+        float bound = 0.f;  // fp16: of |S|
+        bool ok = true;
         uint64_t st[32];  // features 2 c, 2 c + 1 of z
 #pragma unroll
         for (int c = 0; c < 32; ++c) st[c] = 0ull;
@@ -521,7 +563,11 @@ __global__ void __launch_bounds__(1024, 1)
         }
         // row a of the state's 16-bit copy: eight 16-byte pieces placed by the
         // 128-byte swizzle (piece j at j ^ (a mod 8))
-        auto store_copy = [&]() {
+        auto store_copy = [&](int i) {
+            if constexpr (!BF16) {  // by a power of two, which leaves with the scale
+                copy = fp16_up(bound);
+                if (warp == 20 && lane == 0) sd[i & 1] = (rev ? 1.f : p.scale) * fp16_down(copy);
+            }
             if (a < D) {
                 uint8_t* srow = gbase + C::OFF_S + a * 128;
                 const uint64_t c2 = f2(copy, copy);
@@ -539,10 +585,28 @@ __global__ void __launch_bounds__(1024, 1)
             fence_proxy_async_smem();
             mbar_arrive(DBAR(C::B_SSF));
         };
-        if constexpr (!STATE) store_copy();
-        bool ok = true;
+        if (!BF16 && !STATE && (p.nseg > 1 || ps.init)) {
+            // the largest |S| to begin with: the warps meet once
+            float top = 0.f;  // (a maximum passes over NaN)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float2 f = unf2(st[c]);
+                top = max3(top, fabsf(f.x), fabsf(f.y));
+            }
+            const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            float4* sm = reinterpret_cast<float4*>(gbase + C::OFF_SM);
+            if (lane == 0) {
+                (&sm->x)[warp & 3] = __uint_as_float(bits);
+                mbar_arrive(DBAR(C::B_SM));
+            }
+            ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_SM), 0, abort_flag));
+            const float4 m = *sm;
+            bound = fmaxf(max3(m.x, m.y, m.z), m.w);
+            if (isinf(bound)) bound = 16384.f;  // an infinity: the state as it is
+        }
+        if constexpr (!STATE) store_copy(0);
         const double full = exp(ld * kDecayChunk);
-        for (int i = 0; i < nch; ++i) {
+        for (int i = 0; ok && i < nch; ++i) {
             // the sums of step i into the state: S <- L^n S + sums, L^n as a pair of
             // floats so that its error does not add up over the chunks
             if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_KVF + (i & 1)), (i >> 1) & 1, abort_flag))))
@@ -551,6 +615,7 @@ __global__ void __launch_bounds__(1024, 1)
             const double gd = tokens(i) == kDecayChunk ? full : exp(ld * tokens(i));
             const float gf = static_cast<float>(gd);
             const uint64_t g = f2(gf, gf), g2 = f2(static_cast<float>(gd - gf), static_cast<float>(gd - gf));
+            float largest = 0.f;  // times 2^15 a bound of |Z| times its scale
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
                 uint32_t v[NP][16];
@@ -558,6 +623,7 @@ __global__ void __launch_bounds__(1024, 1)
                 for (int k = 0; k < NP; ++k) tmem_ld16(lane_addr + C::COL_KV + 64u * k + 16u * cc, v[k]);
                 const float2 down = BF16 ? make_float2(1.f, 1.f)
                                          : *reinterpret_cast<const float2*>(zd + (i & 3) * 8 + 2 * cc);
+                if (!BF16) largest = max3(largest, down.x, down.y);
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < NP; ++k)
@@ -568,12 +634,15 @@ __global__ void __launch_bounds__(1024, 1)
                     uint64_t sum = f2(__uint_as_float(v[NP - 1][2 * e]), __uint_as_float(v[NP - 1][2 * e + 1]));
 #pragma unroll
                     for (int k = NP - 2; k >= 0; --k)  // the small pieces first
-                        sum = fma2(sum, f2(1.f / C::PIECE_UP, 1.f / C::PIECE_UP),
-                                   f2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])));
+                        sum = add2(sum, f2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])));
                     if (!BF16) sum = mul2(sum, e < 4 ? f2(down.x, down.x) : f2(down.y, down.y));
                     uint64_t& x = st[8 * cc + e];
                     x = fma2(g, x, fma2(g2, x, sum));
                 }
+            }
+            if constexpr (!BF16 && !STATE) {
+                // an entry of the sums: 128 terms of |Y| and |Zh| at most
+                bound = fmaf(gf, bound, 0x1p22f * largest * sy[i & 3]);
             }
             tc_fence_before();
             mbar_arrive(DBAR(C::B_KVE));
@@ -581,7 +650,7 @@ __global__ void __launch_bounds__(1024, 1)
                 // the copy was last read by X S of this step
                 if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_QSD + (i & 1)), (i >> 1) & 1, abort_flag))))
                     break;
-                store_copy();
+                store_copy(i + 1);
             }
         }
         float* last = STATE ? p.seg + seg_mat : (p.nseg == 1 && ps.last ? ps.last + mat : nullptr);
@@ -606,6 +675,43 @@ __global__ void __launch_bounds__(1024, 1)
             const int s = i & 1, n = tokens(i);
             uint8_t* zt = gbase + s * C::STAGE + C::XB + C::YB;
             uint8_t* ht = gbase + C::OFF_ZH;
+            if constexpr (!BF16 && !STATE) {
+                // survey, before Z lands: the largest |X| and |Y|, 16 tokens a warp (rows of 128
+                // bytes, whatever their pieces' order: lane = row mod 4, piece)
+                if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_XF + s), (i >> 1) & 1, abort_flag) &&
+                                                 wait_bounded(DBAR(C::B_YF + s), (i >> 1) & 1, abort_flag)))
+                    break;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int row = (warp - 24) * 16 + (lane >> 3);
+                    const uint8_t* src = gbase + s * C::STAGE + k * C::XB + (warp - 24) * 2048 + lane * 16;
+                    __half2 m[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.f);  // (their maximum passes over NaN)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (row + 4 * u < n) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(src + h * 16384 + u * 512);
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    m[e] = __hmax2(m[e], __habs2(*reinterpret_cast<const __half2*>(&w[e])));
+                            }
+                        }
+                    const float2 f = __half22float2(__hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3])));
+                    const float top = fminf(fmaxf(f.x, f.y), 65504.f);  // an infinity as fp16's largest
+                    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                    if (lane == 0) {
+                        if (k == 0)
+                            sx[(i & 3) * 8 + warp - 24] = __uint_as_float(bits);
+                        else
+                            atomicMax(reinterpret_cast<uint32_t*>(sy + (i & 3)), bits);
+                    }
+                }
+                if (lane == 0) mbar_arrive(DBAR(C::B_SV + s));
+            }
             // Z landed
             bool ok = wait_bounded(DBAR(C::B_ZF + s), (i >> 1) & 1, abort_flag);
             uint4 in[4];
@@ -643,7 +749,7 @@ __global__ void __launch_bounds__(1024, 1)
                 }
                 const float down = up;
                 up = fp16_up(__uint_as_float(top));
-                if (lane == 0) zd[(i & 3) * 8 + piece(0)] = down / up;
+                if (lane == 0) zd[(i & 3) * 8 + piece(0)] = top > 0u ? down * fp16_down(up) : 0.f;
             }
             // the previous product has read Zh
             ok = ok && (i == 0 || wait_bounded(DBAR(C::B_KVF + (s ^ 1)), ((i - 1) >> 1) & 1, abort_flag));
@@ -651,6 +757,8 @@ __global__ void __launch_bounds__(1024, 1)
                 ok = ok && wait_bounded(DBAR(C::B_YF + s), (i >> 1) & 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             if constexpr (BF16) load_z();
+            // the survey's slot of two steps on, last read for two steps back
+            if (!BF16 && !STATE && warp == 24 && lane == 0) sy[(i + 2) & 3] = 0.f;
             const uint64_t minus = f2(-1.f, -1.f);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -669,7 +777,6 @@ __global__ void __launch_bounds__(1024, 1)
                         out[k][e] = pack2<BF16>(x.x, x.y);
                         const float2 h = unpack2<BF16>(out[k][e]);
                         f = fma2(f2(h.x, h.y), minus, f);
-                        if (!BF16) f = mul2(f, f2(C::PIECE_UP, C::PIECE_UP));
                     }
                 }
 #pragma unroll

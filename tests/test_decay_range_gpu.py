@@ -4,10 +4,11 @@ against a 64-bit form.
 
 Tolerances, relative L2 per head.
   States are fp32.  Their terms reach the tensor cores in 16-bit pieces that hold 22
-bits of them (fp16) or 24 (bf16), 2^-23 at most; the fp32 sums over a chunk's 128 tokens
-round 128 times, independently, sqrt(128) 2^-24 = 2^-20.5 of them; each chunk adds two
-roundings and the powers of the decay a few units of 2^-24.  Squares added: below
-STATE_TOL = 2^-20 for a few dozen chunks that count (a rounding ages with its chunk).
+bits of them (fp16, 2^-22 of a term at most, where it is above 2^-17 of its chunk's
+largest) or 24 (bf16); the fp32 sums over a chunk's 128 tokens round 128 times,
+independently, sqrt(128) 2^-24 = 2^-20.5 of them; each chunk adds two roundings and the
+powers of the decay a few units of 2^-24.  Squares added: below STATE_TOL = 2^-20 for a few
+dozen chunks that count (a rounding ages with its chunk).
   16-bit results pass three roundings of half a step in L2, eps / 2 together (as in
 test_decay_gpu): the power-of-two factors that keep fp16 operands in its normal range
 round nothing, so the same holds for small and large operands, while the results are
@@ -170,3 +171,103 @@ SIZES = {
     "gradients of states past 65504": ((60, 1e-3, 1e-3, 1500), 1e-3, 1e6),
     "a small state": ((300, 1e-3, 1e-3, 300), 1e-6, 1e-3),
 }
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sizes", SIZES.values(), ids=SIZES.keys())
+def test_fp16_results_of_small_and_large_operands(sizes, d):
+    by, state, dstate = sizes
+    for N, seed in ((200, 73), (1300, 74)):
+        xs, (s0, ds) = scaled(seed, N, d, "fp16", by)
+        check_all(xs, s0 * state, ds * dstate, torch.tensor([-0.05, -0.6, -0.004], device="cuda"), "fp16")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp16_rows_of_many_sizes(d):
+    """Tokens whose q, k and v differ by up to 2^12 each (results reach 5e4): every row of
+    the result is right by itself.  Its error is that of the result's own rounding, of its
+    weights P_ij, each up to eps / 2 of itself and so eps / 2 sqrt(sum_j P_ij^2 |v_j|^2) in
+    L2, and of the state's copy, eps / 2 of each entry, scale L^t sqrt(sum_a q_a^2 |S_a|^2);
+    few terms may make up a row, so three times the L2 of the three, and half a step of
+    fp16's subnormal numbers.  (Relative to the row itself there is no bound: q S may
+    cancel.)  Weights and entries far below the chunk's largest possible ones are off by
+    2^-39 of those, d scale max|q| max|k| and the largest possible state, instead."""
+    B, H, N = 1, 3, 700
+    (q, k, v, do), (s0, ds) = inputs(B, H, N, d, "bf16", 80)
+    g = torch.Generator().manual_seed(81)
+    q, k, v, do = ((x.float() * torch.exp2(torch.randint(-6, 7, (B, H, N, 1), generator=g).float().cuda())).half()
+                   for x in (q, k, v, do))
+    v, do = v * 2.0 ** -6, do * 2.0 ** -6
+    ld = torch.tensor([-0.05, -1.5, -0.0004], device="cuda")
+    check_all((q, k, v, do), s0, ds, ld, "fp16")
+    o, _ = attn.decay_forward(q, k, v, ld, state=s0)
+    x, y, z, g = q.double(), k.double(), v.double(), ld.double().view(1, H, 1, 1)
+    S, scale = s0.double(), 1 / math.sqrt(d)
+    most = S.abs().amax((2, 3))
+    for c in range(0, N, 128):
+        cut = slice(c, min(N, c + 128))
+        want, after = chunked(x[:, :, cut], y[:, :, cut], z[:, :, cut], ld.double(), S,
+                              ints([cut.stop - c]).long(), scale)
+        i = torch.arange(cut.stop - c, device="cuda", dtype=torch.float64)
+        gap = i[:, None] - i[None]
+        P = x[:, :, cut] @ y[:, :, cut].transpose(2, 3) * torch.where(gap >= 0, torch.exp(g * gap.clamp(min=0)), 0.0)
+        size = (P ** 2) @ (z[:, :, cut] ** 2).sum(-1, keepdim=True) + \
+            torch.exp(g * (i + 1).view(1, 1, -1, 1)) ** 2 * ((x[:, :, cut] ** 2) @ (S ** 2).sum(-1, keepdim=True))
+        big = [a[:, :, cut].abs().amax((2, 3)) for a in (x, y, z)]
+        least = 2.0 ** -39 * scale * (d * big[0] * big[1] * z[:, :, cut].norm(dim=(2, 3)) +
+                                      x[:, :, cut].norm(dim=3).amax(2) * math.sqrt(d) * most)
+        tol = 3 * half("fp16") * torch.sqrt((want ** 2).sum(-1) + scale ** 2 * size[..., 0]) + least[..., None] + \
+            2.0 ** -25 * math.sqrt(d)
+        off = (o[:, :, cut].double() - want).norm(dim=-1)
+        assert (off <= tol).all(), (c, float((off / tol).max()))
+        S, most = after, most + 128 * big[1] * big[2]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_past_the_end_have_no_say(dtype, d):
+    """The largest finite numbers in the rows behind a sequence's last change nothing."""
+    B, H, N, lens = 3, 2, 300, [130, 299, 7]
+    xs, (s0, ds) = inputs(B, H, N, d, dtype, 75)
+    xs = [x * 1e-3 for x in xs]
+    ld = torch.tensor([-0.01, -0.3], device="cuda")
+    calls = []
+    for junk in (0.0, torch.finfo(xs[0].dtype).max, math.inf):
+        for x in xs:
+            for b, n in enumerate(lens):
+                x[b, :, n:] = junk
+        q, k, v, do = xs
+        calls.append([*attn.decay_forward(q, k, v, ld, state=s0, lens=ints(lens)),
+                      *attn.decay_backward(q, k, v, ld, do, state=s0, dstate=ds, lens=ints(lens))])
+    for other in calls[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(calls[0], other))
+    assert all(torch.isfinite(x.float()).all() for x in calls[0])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_an_element_that_is_not_finite_stays_where_it_belongs(bad, dtype):
+    """In a query it spoils that row; in a value its feature of the state, and of the
+    rows from its chunk on; nothing else."""
+    d, N = 128, 400
+    (q, k, v, _), (s0, _) = inputs(1, 2, N, d, dtype, 76)
+    ld = torch.tensor([-0.01, -0.3], device="cuda")
+    n = ints([N]).long()
+    args = [x.double() for x in (q, k, v)]
+    want_o, want_s = chunked(*args, ld.double(), s0.double(), n, 1 / math.sqrt(d))
+    broken = q.clone()
+    broken[0, 0, 150, 3] = bad
+    o, s1 = attn.decay_forward(broken, k, v, ld, state=s0)
+    assert not torch.isfinite(o[0, 0, 150].float()).any()
+    rows = torch.arange(N, device="cuda") != 150
+    near(o[:, :, rows], want_o[:, :, rows], dtype, "o")
+    assert rel(s1, want_s) <= STATE_TOL
+    broken = v.clone()
+    broken[0, 1, 200, 70] = bad
+    o, s1 = attn.decay_forward(q, k, broken, ld, state=s0)
+    cols = torch.arange(d, device="cuda") != 70
+    assert not torch.isfinite(s1[0, 1, :, 70]).any() and not torch.isfinite(o[0, 1, 256:, 70].float()).any()
+    assert torch.isfinite(s1[..., cols]).all() and torch.isfinite(o[0, 0].float()).all()
+    near(o[..., cols], want_o[..., cols], dtype, "o")
+    assert rel(s1[..., cols], want_s[..., cols]) <= STATE_TOL
+    near(o[:, 1:, :128], want_o[:, 1:, :128], dtype, "o")  # the chunks in front of it
