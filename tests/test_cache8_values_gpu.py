@@ -142,3 +142,36 @@ def test_attention_of_a_query_of_nan_is_nan(Hq, T, lens):
     assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
     assert torch.equal(o[0], first[0]) and torch.equal(lse[0], first[1])
     assert attn.attn_last_device_status() == 0
+
+
+@pytest.mark.parametrize("d,Hq,dtype", [(64, 40, "bf16"), (128, 40, "fp16")])
+def test_attend_tiles_over_thousands_of_keys_a_cta(d, Hq, dtype):
+    """A bound of the lengths that is far too low leaves the last split of the
+    tensor-memory tiles more than 64 tiles: pages and scales looked up in batches of 32
+    tiles, each page with a scale of its own, a bad page right behind a batch's end."""
+    page, n = 16, 9100
+    P, table = tables(1, -(-n // page), 60)
+    cache = filled_cache(P, 1, page, d, 61, spread=6)
+    q = torch.randn(1, Hq, 1, d, generator=torch.Generator().manual_seed(62)).to(TYPES[dtype]).cuda()
+    whole = check_attend(q, cache, table, [n])
+    check_attend(q, cache, table, [n], max_len=600)
+    check_attend(q, cache, table, [n - 13], max_len=1)  # one split
+    for entry in (512 // 16 + 32 * 8, 512 // 16 + 32 * 8 - 1, 32 * 8, 64 * 8 + 3):
+        table[0, entry] = P + 5
+    check_attend(q, cache, table, [n], max_len=600, bad=True)
+    check_attend(q, cache, table, [n], max_len=1, bad=True)
+    again = attn.cache_attend(q, cache, table.clamp(max=P - 1), ints([n]))  # the same sizes still run
+    assert attn.attn_last_device_status() == 0 and again[0].shape == whole[0].shape
+
+
+@pytest.mark.parametrize("Hq,Hkv,T,n", [(16, 16, 1, 4096), (32, 8, 1, 3000), (16, 2, 5, 5001), (8, 1, 1, 700)])
+def test_calls_repeat_themselves_bit_for_bit(Hq, Hkv, T, n):
+    page, d, B = 64, 128, 4
+    P, table = tables(B, -(-n // page), 63)
+    cache = filled_cache(P, Hkv, page, d, 64)
+    q = torch.randn(B, Hq, T, d, generator=torch.Generator().manual_seed(65)).bfloat16().cuda()
+    lens = ints([n, n // 2, n // 3, T])
+    want = [x.clone() for x in attn.cache_attend(q, cache, table, lens)]
+    for _ in range(20):
+        for a, b in zip(attn.cache_attend(q, cache, table, lens), want):
+            assert torch.equal(a, b)

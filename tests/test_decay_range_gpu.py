@@ -271,3 +271,39 @@ def test_an_element_that_is_not_finite_stays_where_it_belongs(bad, dtype):
     near(o[..., cols], want_o[..., cols], dtype, "o")
     assert rel(s1[..., cols], want_s[..., cols]) <= STATE_TOL
     near(o[:, 1:, :128], want_o[:, 1:, :128], dtype, "o")  # the chunks in front of it
+
+
+@pytest.mark.parametrize("B,H,N,d,dtype,lens", [
+    (1, 3, 9000, 64, "bf16", None), (1, 3, 9000, 128, "fp16", None), (2, 3, 5000, 128, "bf16", [4999, 2049]),
+    (2, 3, 5000, 64, "fp16", [1, 4100])])
+def test_long_sequences_and_slow_decays(B, H, N, d, dtype, lens):
+    """Dozens of chunks in one segment or several, memories of thousands of tokens: the
+    states would lose their precision with one 32-bit decay a chunk."""
+    xs, (s0, ds) = inputs(B, H, N, d, dtype, 77)
+    for x in xs:
+        for b, n in enumerate(lens or []):
+            x[b, :, n:] = 0
+    check_all(xs, s0, ds, torch.tensor(SLOW, device="cuda"), dtype, lens)
+
+
+def test_large_heads_against_the_64_bit_form():
+    """The large-head shape, a walk of 32 chunks for each of 64 heads."""
+    B, H, N, d = 4, 16, 4096, 128
+    xs, (s0, ds) = inputs(B, H, N, d, "bf16", 78)
+    ld = torch.tensor([SLOW[h % 3] * (1 + h) for h in range(H)], device="cuda")
+    check_all(xs, s0, ds, ld, "bf16", heads=slice(0, 16, 5))
+
+
+@pytest.mark.parametrize("N", [300, 4000])
+def test_calls_repeat_themselves_bit_for_bit(N):
+    xs, (s0, ds) = inputs(2, 4, N, 64, "fp16", 79)
+    q, k, v, do = xs
+    ld = torch.tensor([*SLOW, -1.0], device="cuda")
+    step = [x[:, :, :1].contiguous() for x in (q, k, v)]
+
+    def run():
+        return [*attn.decay_forward(q, k, v, ld, state=s0), *attn.decay_step(*step, ld, s0),
+                *attn.decay_backward(q, k, v, ld, do, state=s0, dstate=ds)]
+    want = run()
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(run(), want))
