@@ -453,8 +453,9 @@ def _cache_shape(k, v, ks, vs, d, page_table, lens, B):
 
 
 def _check_workspace(workspace, need):
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        raise ValueError(f"workspace needs {need} bytes")
+    if need and (workspace is None or not workspace.is_contiguous()
+                 or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace needs {need} contiguous bytes")
 
 
 def attn_cache_append(k, v, cache: Cache8, page_table, lens, n_new=None, stream=None) -> None:
