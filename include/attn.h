@@ -286,8 +286,8 @@ int attn_linear_fwd(const void* q, const void* k, const void* v, void* o, void* 
  * attn_cache_attend_workspace_bytes() bytes of the same sizes and max_len, 16-byte
  * aligned (may be NULL when that is 0); its contents on entry do not matter.
  *
- * Errors: as attn_fwd; ATTN_ERR_ARG for another page size, max_len < 1, or K
- * and V in one array; ATTN_ERR_SHAPE if Hkv does not divide Hq.  Contents of
+ * Errors: as attn_fwd; ATTN_ERR_ARG for another page size, max_len < 1, or an
+ * append of K and V into one array; ATTN_ERR_SHAPE if Hkv does not divide Hq.  Contents of
  * the int32 arrays are checked on the device: a page index outside 0 ..
  * num_pages - 1, a length below 0 or past max_pages * page, or n_new / q_lens
  * outside 0 .. T is never followed: its tokens are not stored (append) or not
