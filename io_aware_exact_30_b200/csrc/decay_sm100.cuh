@@ -108,16 +108,16 @@ __device__ __forceinline__ void decay_span(int n, int seg, int seg_chunks, int* 
 //       max|Y| max|Z| a chunk, as the state's own rounding errors do; likewise
 // The maxima of X and Y are surveyed by the Zh warps, before Z lands.  (Exact maxima of P,
 // over which the four warps of the same rows meet: 12 heads of 23400 tokens 84 us; the survey
-// by a warp of its own 82, by the state warps 94; as it is 73; without P's and S's powers 65.)
+// by a warp of its own 82, by the state warps 94; as it is 71; without P's and S's powers 65.)
 //
 // What bounds it: the chain of the roles from one chunk to the next, 4700 cycles of it at
 // D = 128 (2.4 us a chunk), in which a role waits for what another hands over.  The
 // products take about 2150 cycles of the tensor pipe; the operands they read, the loads,
 // Zh, the state's copy and the staged result about 3100 cycles of shared-memory bandwidth.
 // HBM would allow 1.3 us.
-// Measured (one B200, device time): 4 x 16 heads of 4096 tokens, d = 128, bf16: 85 us
-// (269 MB and states: 3.2 TB/s), the gradients 236 us; 12 heads of 23400 tokens,
-// d = 64, fp16, in 12 segments: 64 us.  The same kernel without Zh, P and stores: 57 us.
+// Measured (one B200, device time of a replayed graph): 4 x 16 heads of 4096 tokens, d =
+// 128, bf16: 86 us (269 MB and states: 3.1 TB/s), the gradients 235 us; 12 heads of 23400
+// tokens, d = 64, fp16, in 12 segments: 71 us.  The first without Zh, P and stores: 57 us.
 //
 // Roles (eight warpgroups, 1024 threads): warp 0 loads (TMA), warp 1 issues the
 // products, warp 2 stores (TMA), 3 fills rows past the end; 16 warps make P and the
@@ -173,7 +173,7 @@ struct DecayCfg {
     // registers of a thread by role; the launch gives each of the eight warpgroups 64
     static constexpr int R_ISSUE = BF16 ? 32 : 40, R_ROW = 56, R_STATE = BF16 ? 144 : 136, R_ZH = 56;
     static_assert(R_ISSUE + 4 * R_ROW + R_STATE + 2 * R_ZH <= 8 * 64, "more registers than the launch has");
-    static_assert(R_ISSUE <= 64 && R_ROW <= 64 && R_ZH <= 64 && R_STATE >= 64, "a share on the wrong side of the launch's");
+    static_assert(R_ISSUE <= 64 && R_ROW <= 64 && R_ZH <= 64 && R_STATE >= 64, "a share on the launch's wrong side");
     static_assert(SMEM_BYTES <= 232448u, "dynamic shared memory above the sm_100 per-block limit");
 };
 
@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(1024, 1)
             const int rows = i == C::B_PF || i == C::B_OE || i == C::B_OW || i == C::B_OW + 1;
             const int state = i == C::B_KVE || i == C::B_SSF;
             mbar_init(DBAR(i), rows ? C::NROW
-                                    : (state ? C::NSTATE : (i == C::B_ZH ? C::NZH : (i == C::B_SM ? 4 : (i >= C::B_SV ? 8 : 1)))));
+                                    : (state ? C::NSTATE
+                                             : (i == C::B_ZH ? C::NZH : (i == C::B_SM ? 4 : (i >= C::B_SV ? 8 : 1)))));
         }
         *abort_flag = 0u;
         if (!BF16)
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(1024, 1)
             tc_fence_before();
             mbar_arrive(DBAR(C::B_PF));
             // in a buffer of its own the previous step's output is staged during P Z
-            // (12 heads of 23400 tokens: 64.2 to 62.9 us)
+            // (12 heads of 23400 tokens, before the powers of two: 64.2 to 62.9 us)
             if (C::OWN_O && i >= 1 && !(ok = stage(i - 1))) break;
             if (!(ok = __all_sync(0xffffffffu, wait_bounded(DBAR(C::B_OD + b), (i >> 1) & 1, abort_flag)))) break;
             tc_fence_after();
@@ -681,34 +682,40 @@ __global__ void __launch_bounds__(1024, 1)
                 if (!__all_sync(0xffffffffu, wait_bounded(DBAR(C::B_XF + s), (i >> 1) & 1, abort_flag) &&
                                                  wait_bounded(DBAR(C::B_YF + s), (i >> 1) & 1, abort_flag)))
                     break;
+                const int row = (warp - 24) * 16 + (lane >> 3);
+                const uint8_t* src = gbase + s * C::STAGE + (warp - 24) * 2048 + lane * 16;
+                __half2 m[2][2];  // (a maximum passes over NaN)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e >> 1][e & 1] = __float2half2_rn(0.f);
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    uint4 x[8];  // all loads before the first is used
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        x[u] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row + 4 * (u & 3) < n)
+                            x[u] = *reinterpret_cast<const uint4*>(src + (u >> 2) * C::XB + h * 16384 + (u & 3) * 512);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m[u >> 2][e & 1] =
+                                __hmax2(m[u >> 2][e & 1], __habs2(*reinterpret_cast<const __half2*>(&w[e])));
+                    }
+                }
+                uint32_t top[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int row = (warp - 24) * 16 + (lane >> 3);
-                    const uint8_t* src = gbase + s * C::STAGE + k * C::XB + (warp - 24) * 2048 + lane * 16;
-                    __half2 m[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.f);  // (their maximum passes over NaN)
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (row + 4 * u < n) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(src + h * 16384 + u * 512);
-                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    m[e] = __hmax2(m[e], __habs2(*reinterpret_cast<const __half2*>(&w[e])));
-                            }
-                        }
-                    const float2 f = __half22float2(__hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3])));
-                    const float top = fminf(fmaxf(f.x, f.y), 65504.f);  // an infinity as fp16's largest
-                    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-                    if (lane == 0) {
-                        if (k == 0)
-                            sx[(i & 3) * 8 + warp - 24] = __uint_as_float(bits);
-                        else
-                            atomicMax(reinterpret_cast<uint32_t*>(sy + (i & 3)), bits);
-                    }
+                    const __half2 a = __hmax2(m[k][0], m[k][1]);
+                    top[k] = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(__half_as_ushort(
+                                                                __hmax(__low2half(a), __high2half(a)))));
+                }
+                if (lane == 0) {  // (an infinity as fp16's largest)
+                    sx[(i & 3) * 8 + warp - 24] = unpack2<false>(min(top[0], 0x7bffu)).x;
+                    atomicMax(reinterpret_cast<uint32_t*>(sy + (i & 3)),
+                              __float_as_uint(unpack2<false>(min(top[1], 0x7bffu)).x));
                 }
                 if (lane == 0) mbar_arrive(DBAR(C::B_SV + s));
             }
@@ -864,7 +871,7 @@ __global__ void __launch_bounds__(128) decay_scan_kernel(const __grid_constant__
 // Segments of a call: one, unless its CTAs (one per pass, head and 64 features)
 // fill less than half of the device's 148 multiprocessors; then as many as fit,
 // of four chunks at least (a segment costs a second pass over y and z, and a
-// state written and read: 12 heads of 23400 tokens, d = 64, take 64 us in 12
+// state written and read: 12 heads of 23400 tokens, d = 64, take 71 us in 12
 // segments; 183 chunks in a row are 370 us at the 2 us each that a long walk takes).
 inline void decay_segments(int B, int H, int N, int d, int passes, int* nseg, int* seg_chunks) {
     const long long ctas = 1LL * passes * B * H * (d / 64);
