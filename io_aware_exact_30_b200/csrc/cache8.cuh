@@ -52,8 +52,9 @@ struct AppendParams {
 // found; it decides the scale, and the rows are stored as codes.
 //
 // Bound by HBM for prompts (2 bytes read, 1 written per value: four of up to 4096
-// tokens, 16 heads, d = 128: 26 us, 5.5 TB/s) and by the launch and two dependent
-// loads for single tokens (64 sequences, 8 heads: 4.5 us).
+// tokens, 16 heads, d = 128: 26 us, 5.5 TB/s), for single tokens by the launch, two
+// dependent loads and the parameters' copy in local memory, which the choice of K's or V's
+// array at run time brings (64 sequences, 8 heads: 4.5 us).
 template <int D, bool BF16, int NCH>
 __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p) {
     constexpr int PER_ROW = D / 8;  // 16-byte pieces of a row
@@ -268,7 +269,8 @@ __device__ __forceinline__ void attend_lengths(const AttendParams& p, int b, int
 // registers): 64 sequences of 2.7 to 8 thousand tokens, 8 key/value heads, d = 128:
 // 155 us, 4.6 TB/s (5 CTAs an SM at 96 registers: 184; 3 at 150: 159; the query rows in
 // the wide extent of the fragments, 16 of which a single token fills one: 239).  Few
-// heads: the launch, four dependent loads and the join: 16 heads of 4096 tokens 12.5 us.
+// heads: the launch, four dependent loads and the join, about half of the time by estimate
+// (no breakdown was taken): 16 heads of 4096 tokens 12.5 us.
 // 16 rows convert the codes once for two fragments: 60 us for 16 x 2 heads of 16000
 // tokens where 8 rows take 37.
 template <int D, int NT>

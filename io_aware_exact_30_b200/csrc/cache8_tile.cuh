@@ -21,7 +21,8 @@
 // joined at the end: their warps never wait for one another.
 //
 // What bounds it: the softmax warps' chain (64 keys of a row a thread: about 2000
-// cycles a tile, its exponentials alone 1000), where the products take 1024 and a
+// cycles a tile, its exponentials alone 1000), which the lanes of the low pieces go
+// through a second time, where the products take 1024 and a
 // tile's 32 KB of codes 1400 of a multiprocessor's share of HBM; and 8 us before a CTA's
 // first tile and after its last.  Measured: five queries of 8 heads a key/value head
 // over 16 sequences of 5 to 16 thousand tokens, d = 128: 64 us (16-row fragments, which
