@@ -307,3 +307,48 @@ def test_calls_repeat_themselves_bit_for_bit(N):
     want = run()
     for _ in range(10):
         assert all(torch.equal(a, b) for a, b in zip(run(), want))
+
+
+@pytest.mark.parametrize("N", [140, 1700])
+def test_fp16_decays_at_their_ends(N):
+    """A NaN decay makes its head NaN, no memory at all and a steep one stay right, in one
+    segment and several."""
+    xs, (s0, ds) = inputs(1, 4, N, 64, "fp16", 82)
+    q, k, v, do = xs
+    ld = torch.tensor([-0.1, math.nan, -math.inf, -1.7], device="cuda")
+    o, s1 = attn.decay_forward(q, k, v, ld, state=s0)
+    grads = attn.decay_backward(q, k, v, ld, do, state=s0, dstate=ds)
+    assert attn.attn_last_device_status() == 0
+    for x in (o, s1, *grads):
+        assert torch.isnan(x[:, 1]).all()
+    keep = [0, 2, 3]
+    want_o, want_s, want = gradients(*(x[:, keep] for x in (q, k, v)), torch.nan_to_num(ld[keep], neginf=-1e4),
+                                     do[:, keep], s0[:, keep], ds[:, keep], ints([N]).long(), 1 / math.sqrt(64))
+    near(o[:, keep], want_o, "fp16", "o")
+    for name, a, w in zip(("dq", "dk", "dv"), grads, want):
+        near(a[:, keep], w, "fp16", name)
+    assert rel(s1[:, keep], want_s) <= STATE_TOL
+    dead = want[3].abs().amax((2, 3)) == 0  # (nothing of the first state is left)
+    assert (grads[3][:, keep][dead] == 0).all()
+    left = [h for i, h in enumerate(keep) if not dead[0, i]]
+    if left:
+        assert rel(grads[3][:, left], want[3][:, [i for i in range(3) if not dead[0, i]]]) <= STATE_TOL
+
+
+def test_two_calls_at_once_do_not_share_anything():
+    ld = torch.tensor([*SLOW, -1.0], device="cuda")
+    sets = [inputs(1, 4, N, 128, "fp16", 83 + N) for N in (1500, 900)]
+    run = lambda xs, st: [*attn.decay_forward(*xs[:3], ld, state=st[0]),  # noqa: E731
+                          *attn.decay_backward(*xs[:3], ld, xs[3], state=st[0], dstate=st[1])]
+    want = [[x.clone() for x in run(*s)] for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for s, side in zip(sets, streams):
+            with torch.cuda.stream(side):
+                got.append(run(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert attn.attn_last_device_status() == 0
